@@ -450,6 +450,155 @@ PA_API pa_status pa_fp4_logits(const pa_fp4_problem *p, const uint8_t *q, const 
                                const int32_t *block_table, void *workspace, size_t workspace_bytes,
                                void *out, pa_stream_t stream);
 
+/* Attention over whole prompts: packed sequences of different lengths with
+ * grouped heads -- the step that comes before the first pa_insert of a
+ * request, or (with cached keys gathered in front) the next chunk of one.
+ *
+ * Sequence s has query tokens cu_q[s] .. cu_q[s + 1] - 1 and key tokens
+ * cu_k[s] .. cu_k[s + 1] - 1 of the packed rows, lq and lk of them.  For its
+ * query token i, query head h and kv head g = h / (Hq / Hkv):
+ *
+ *   vis   = causal ? i + 1 + lk - lq : lk       (the ends of both are aligned)
+ *   out   = softmax_t( softmax_scale * q[i, h, :] . k[t, g, :] ) . v[t, g, :]   for t < vis
+ *   lse   = ln sum_t exp(softmax_scale * q . k)                       (optional)
+ *   vis <= 0 gives out = 0 and lse = -inf.
+ *
+ * Keys and values at t >= vis never reach the row, whatever they hold (NaN and
+ * infinities included).  The softmax weights are rounded once to the dtype of
+ * v before they multiply it (its sum is taken unrounded, in fp32); scores, row
+ * maxima, sums and outputs are accumulated in fp32.
+ *
+ * Arguments (device pointers unless stated):
+ *  p         host.
+ *  q         [total_q] rows of [Hq][D], q_stride elements apart; k, v
+ *            [total_k] rows of [Hkv][D], k_stride / v_stride elements apart (so
+ *            the three may be slices of one fused projection).  Base addresses
+ *            and strides are multiples of 16 bytes.
+ *  cu_q, cu_k  [num_seqs + 1] int32 prefix sums: 0 <= cu[s] <= cu[s + 1] <=
+ *            total.  Rows that no sequence names are neither read into a
+ *            result nor written.
+ *  out       [total_q][Hq][D] of out_dtype, contiguous, 16-byte aligned.
+ *  lse       optional [total_q][Hq] fp32, or NULL.
+ *  dev_error optional device uint32 that the kernel ORs error bits into (read
+ *            it with pa_get_error(dev_error, ...)); NULL to ignore.
+ * Supported: head_dim 64, 128 or 256, Hq / Hkv <= 128, softmax_scale > 0,
+ * num_seqs <= 65535, 16-byte-aligned rows; other problems return
+ * PA_ERR_UNSUPPORTED.  A sequence whose prefix sums break the contract
+ * (PA_DEV_ERR_CONTEXT_LEN) gets NaN rows when its query range is valid and no
+ * rows otherwise; a wait that runs out (PA_DEV_ERR_TIMEOUT) leaves NaN rows.
+ * One kernel launch on `stream`, no workspace, no allocation, no
+ * synchronisation; results do not depend on how sequences are packed. */
+typedef struct pa_prompt_problem {
+    int32_t num_seqs;     /* sequences, >= 0 */
+    int32_t total_q;      /* packed query rows */
+    int32_t total_k;      /* packed key rows */
+    int32_t num_q_heads;  /* Hq */
+    int32_t num_kv_heads; /* Hkv, divides Hq */
+    int32_t head_dim;     /* D */
+    int32_t dtype;        /* PA_F16 or PA_BF16: q, k and v */
+    int32_t out_dtype;    /* PA_F32, PA_F16, PA_BF16 */
+    int32_t causal;       /* 1: query token i sees keys t <= i + lk - lq */
+    int32_t q_stride;     /* elements between packed rows; 0 = Hq * D */
+    int32_t k_stride;     /* 0 = Hkv * D */
+    int32_t v_stride;     /* 0 = Hkv * D */
+    float softmax_scale;  /* e.g. 1/sqrt(D) */
+} pa_prompt_problem;
+
+PA_API pa_status pa_prompt_attention(const pa_prompt_problem *p, const void *q, const void *k, const void *v,
+                                     const int32_t *cu_q, const int32_t *cu_k, void *out, float *lse,
+                                     uint32_t *dev_error, pa_stream_t stream);
+
+/* Accumulated attention weight of the cached tokens: how much of the softmax
+ * of the newest query rows each token of the paged cache received, added to a
+ * running total.  This is the score by which pa_evict keeps tokens.
+ *
+ *   mass[b][g][t] = decay * mass[b][g][t]
+ *                   + sum_{j < next_n} sum_{h in group g} [t < vis_bj]
+ *                     exp(softmax_scale * q[b][j][h] . k^_t - lse[b][j][h])
+ *
+ * for 0 <= t < L_b, with vis_bj and k^_t as for pa_run and lse the
+ * log-sum-exps that pa_attention returned for the same rows (any others give
+ * the same formula).  Entries t >= L_b are left as they are.  decay = 0 does
+ * not read mass.  A row whose lse is -inf (it saw nothing) adds nothing.
+ * Scores and weights are fp32; queries and codes enter the tensor cores
+ * exactly (bf16 queries against f16 operands scaled by a power of two, which
+ * drops what is below 2^-24 of a row's largest value; a folded per-channel
+ * scale as a sum of two f16 terms, 22 bits).
+ *
+ * Arguments as for pa_run, plus:
+ *  decay     host, finite.
+ *  lse       device [batch][next_n][Hq] fp32.
+ *  mass      device [batch][Hkv][max_context_len] fp32, updated in place.
+ *  dev_error optional device uint32 that collects error bits, or NULL.
+ * Reads of p: as pa_run but for head_dim_v, out_dtype, v_scale_mode and
+ * v_is_k_prefix (only K is read).  q and k_pool 16-byte aligned.
+ * Supported: head_dim_k 64, 128 or 256 (INT4: 128 or 256), block_size a
+ * multiple of 16; f16 / bf16 codes with no or one scale, E4M3 with any scale
+ * mode (TOKEN: the scales in the blocks), INT8 / INT4 with no, one or
+ * per-channel scales; batch <= 8192; other problems return
+ * PA_ERR_UNSUPPORTED.  A request whose length breaks the contract
+ * (PA_DEV_ERR_CONTEXT_LEN) is left as it is; tokens of a block whose id is
+ * outside [1, num_blocks) get NaN (PA_DEV_ERR_BLOCK_ID).  One kernel launch;
+ * every entry has one writer and a fixed order of additions, so results are
+ * bitwise the same under relocation and from run to run. */
+PA_API pa_status pa_attention_mass(const pa_problem *p, float decay, const void *q, const void *k_pool,
+                                   const int32_t *block_table, const int32_t *context_lens, const float *k_scale,
+                                   const float *lse, float *mass, uint32_t *dev_error, pa_stream_t stream);
+
+/* Eviction from the paged cache by accumulated attention weight.  Every
+ * request keeps left = min(L_b, budget) tokens per kv head, each kv head its
+ * own: the `sinks` first and the `recent` newest ones always, then those of
+ * the largest mass (NaN below everything; ties keep the lower slot).
+ *
+ * The cache stays dense: slots 0 .. left - 1 of the request hold the kept
+ * tokens.  A kept token whose slot is below `left` stays where it is; the
+ * i-th kept token at or past `left` moves into the i-th slot below `left` that
+ * was not kept, codes (and per-token scales) of K and V, mass and position
+ * with it.  That is the smallest number of rows that can move, and none is
+ * read after it was written.  Attention does not depend on the order of
+ * cached tokens (positions are in the keys), and the next tokens append at
+ * slot `left`.
+ *
+ * Since slots are then no longer in order of age, positions are kept beside
+ * the cache: history[b] = {n, dropped} says that the first n slots' original
+ * positions are in positions[b][g][0 .. n) and that slot s >= n holds
+ * position dropped + s.  A cache that nothing was evicted from has
+ * history = {0, 0}.  Token position pos is a sink if pos < sinks, recent if
+ * pos >= L_b + dropped - recent.
+ *
+ * Arguments (device pointers unless stated):
+ *  p             host; batch, num_kv_heads, head_dim_k/v, block_size,
+ *                num_blocks, max_blocks_per_seq, max_context_len, kv_dtype,
+ *                k/v_scale_mode, v_is_k_prefix and num_sms are read.
+ *  budget, sinks, recent  host; budget >= 1, sinks + recent <= budget.
+ *  mass          [batch][Hkv][max_context_len] fp32.
+ *  positions     [batch][Hkv][max_context_len] int32; history [batch][2] int32.
+ *  block_table, context_lens  as for pa_run.
+ *  k_pool, v_pool  the planes, moved in place (v_pool NULL when v_is_k_prefix).
+ *  mass_out      as mass: slots [0, left) the kept tokens' mass, [left, L_b) 0.
+ *  positions_out as positions: slots [0, left); history_out [batch][2]:
+ *                {left, dropped + L_b - left}; lens_out [batch] int32: left.
+ *                Each of the four may be the same buffer as its input; entries
+ *                not named here are left as they are.
+ *  workspace     pa_evict_workspace_size() bytes, 256-byte aligned; word 0 is
+ *                the device error word (pa_get_error).
+ * Blocks that hold moved or filled slots must not be shared between requests.
+ * Rows of whole 16-byte pieces (head_dim * bits / 8) and max_context_len <=
+ * 2^20 are supported; other problems return PA_ERR_UNSUPPORTED.  A request
+ * whose length or history breaks the contract (PA_DEV_ERR_CONTEXT_LEN) or
+ * which has a block id outside [1, num_blocks) (PA_DEV_ERR_BLOCK_ID) is left
+ * unevicted: nothing of it is written but lens_out (its length) and
+ * history_out (its history).  Calls with the same inputs give the same bytes,
+ * and a second call on the moved cache with the same (unchanged) inputs moves
+ * the same rows again.  Two kernel launches, no synchronisation. */
+PA_API pa_status pa_evict_workspace_size(const pa_problem *p, int32_t budget, size_t *bytes);
+
+PA_API pa_status pa_evict(const pa_problem *p, int32_t budget, int32_t sinks, int32_t recent, const float *mass,
+                          const int32_t *positions, const int32_t *history, const int32_t *block_table,
+                          const int32_t *context_lens, void *k_pool, void *v_pool, float *mass_out,
+                          int32_t *positions_out, int32_t *history_out, int32_t *lens_out, void *workspace,
+                          size_t workspace_bytes, pa_stream_t stream);
+
 /* Copy the device error word to *bits.  Synchronises `stream`. */
 PA_API pa_status pa_get_error(const void *workspace, uint32_t *bits, pa_stream_t stream);
 

@@ -5,7 +5,8 @@ include/pa.h; this package is its thin Python face:
 
   * `_binding`  -- ctypes declarations of pa_workspace_size / pa_plan / pa_run /
                    pa_combine / pa_attention / pa_insert / pa_sparse_attention /
-                   pa_fp4_logits / pa_get_error (same names);
+                   pa_fp4_logits / pa_prompt_attention / pa_attention_mass /
+                   pa_evict / pa_get_error (same names);
   * `problem()` / `run()` -- marshal a batch held in torch CUDA tensors into
                    those calls (pointers, sizes, the current stream);
   * `workloads` -- seeded synthetic inputs (no attention arithmetic).
@@ -18,6 +19,7 @@ import math
 from typing import Optional
 
 __all__ = ["problem", "workspace_bytes", "run", "insert", "sparse_run", "fp4_problem", "fp4_logits",
+           "prompt_problem", "prompt_attention", "attention_mass", "evict_workspace_bytes", "evict",
            "stream_handle", "binding"]
 
 
@@ -133,3 +135,106 @@ def fp4_logits(w, p, out, workspace, stream=None) -> None:
     b = binding()
     b.pa_fp4_logits(p, _ptr(w.q), _ptr(w.sf_q), _ptr(w.kv_fused), _ptr(w.weights), _ptr(w.context_lens),
                     _ptr(w.block_table), _ptr(workspace), workspace.numel(), _ptr(out), stream_handle(stream))
+
+
+def _need(t, name: str, dtype=None, numel: int = 0, contiguous: bool = True) -> int:
+    """The address of a CUDA tensor of at least numel elements on the current device, or a ValueError."""
+    import torch
+    if t is None:
+        return None
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: a tensor on the current CUDA device is needed, got {t.device}")
+    if dtype is not None and str(t.dtype) != dtype:
+        raise ValueError(f"{name}: {dtype} is needed, got {t.dtype}")
+    if t.numel() < numel:
+        raise ValueError(f"{name}: {numel} elements are needed, got {t.numel()}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous tensor is needed")
+    return t.data_ptr()
+
+
+_TORCH_OF = {0: "torch.float32", 1: "torch.float16", 2: "torch.bfloat16"}
+
+
+def prompt_problem(*, num_seqs: int, total_q: int, total_k: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                   dtype: str = "bf16", out_dtype: Optional[str] = None, causal: bool = True,
+                   softmax_scale: Optional[float] = None, q_stride: int = 0, k_stride: int = 0, v_stride: int = 0):
+    """pa_prompt_problem for packed prompts: num_seqs sequences of total_q
+    query and total_k key rows in all.  Strides are the elements between rows
+    (0 = contiguous [rows][heads][head_dim]); softmax_scale defaults to
+    1/sqrt(head_dim), out_dtype to dtype."""
+    b = binding()
+    return b.PromptProblem(num_seqs=num_seqs, total_q=total_q, total_k=total_k, num_q_heads=num_q_heads,
+                           num_kv_heads=num_kv_heads, head_dim=head_dim, dtype=b.DTYPE[dtype],
+                           out_dtype=b.DTYPE[out_dtype or dtype], causal=int(bool(causal)), q_stride=q_stride,
+                           k_stride=k_stride, v_stride=v_stride,
+                           softmax_scale=1.0 / math.sqrt(head_dim) if softmax_scale is None else softmax_scale)
+
+
+def prompt_attention(p, q, k, v, cu_q, cu_k, out, lse=None, dev_error=None, stream=None) -> None:
+    """Enqueue pa_prompt_attention: causal (or full) attention of packed
+    prompts.  q [total_q, Hq, D] and k, v [total_k, Hkv, D] (rows q_stride,
+    k_stride, v_stride elements apart, each row contiguous), cu_q and cu_k
+    int32 [num_seqs + 1], out [total_q, Hq, D], lse optional float32
+    [total_q, Hq], dev_error an optional int32 tensor of one element that
+    collects the error bits."""
+    b = binding()
+    dt, D = _TORCH_OF.get(p.dtype), p.head_dim
+
+    def rows(t, name, heads, stride, n):
+        if t.dim() != 3 or tuple(t.shape[1:]) != (heads, D) or t.shape[0] < n or (
+                n > 0 and (t.stride(2) != 1 or t.stride(1) != D)):
+            raise ValueError(f"{name}: [{n}, {heads}, {D}] rows are needed, got {tuple(t.shape)} strides {t.stride()}")
+        if n > 1 and t.stride(0) != (stride or heads * D):
+            raise ValueError(f"{name}: rows {stride or heads * D} elements apart are needed, got {t.stride(0)}")
+        return _need(t, name, dt, contiguous=False)
+
+    b.pa_prompt_attention(p, rows(q, "q", p.num_q_heads, p.q_stride, p.total_q),
+                          rows(k, "k", p.num_kv_heads, p.k_stride, p.total_k),
+                          rows(v, "v", p.num_kv_heads, p.v_stride, p.total_k),
+                          _need(cu_q, "cu_q", "torch.int32", p.num_seqs + 1),
+                          _need(cu_k, "cu_k", "torch.int32", p.num_seqs + 1),
+                          _need(out, "out", _TORCH_OF.get(p.out_dtype), p.total_q * p.num_q_heads * D),
+                          _need(lse, "lse", "torch.float32", p.total_q * p.num_q_heads),
+                          _need(dev_error, "dev_error", "torch.int32", 1), stream_handle(stream))
+
+
+def attention_mass(w, p, lse, mass, decay: float = 1.0, dev_error=None, stream=None) -> None:
+    """Enqueue pa_attention_mass for a workload on the device: add to mass
+    (float32 [B, Hkv, max_context_len]) the softmax weight every cached token
+    receives from the query rows w.q, given their log-sum-exps lse
+    (float32 [B, n, Hq], as pa_attention wrote them)."""
+    b = binding()
+    B, n = p.batch, p.next_n
+    b.pa_attention_mass(p, decay, _need(w.q, "q", _TORCH_OF.get(p.q_dtype), B * n * p.num_q_heads * p.head_dim_k),
+                        _need(w.k_pool, "k_pool"),
+                        _need(w.block_table, "block_table", "torch.int32", B * p.max_blocks_per_seq),
+                        _need(w.context_lens, "context_lens", "torch.int32", B),
+                        _need(w.k_scale, "k_scale", "torch.float32"),
+                        _need(lse, "lse", "torch.float32", B * n * p.num_q_heads),
+                        _need(mass, "mass", "torch.float32", B * p.num_kv_heads * p.max_context_len),
+                        _need(dev_error, "dev_error", "torch.int32", 1), stream_handle(stream))
+
+
+def evict_workspace_bytes(p, budget: int) -> int:
+    return binding().pa_evict_workspace_size(p, budget)
+
+
+def evict(w, p, budget: int, mass, positions, history, mass_out, positions_out, history_out, lens_out, workspace, *,
+          sinks: int = 0, recent: int = 0, stream=None) -> None:
+    """Enqueue pa_evict for a workload on the device: keep, per request and kv
+    head, the first `sinks` and newest `recent` tokens and those of the largest
+    mass, `budget` in all, at the front of w's pools (moved in place).  mass
+    float32 and positions int32 [B, Hkv, max_context_len], history int32
+    [B, 2]; the *_out tensors may be the inputs themselves and lens_out
+    w.context_lens."""
+    b = binding()
+    B, rows = p.batch, p.batch * p.num_kv_heads * p.max_context_len
+    i32, f32 = "torch.int32", "torch.float32"
+    b.pa_evict(p, budget, sinks, recent, _need(mass, "mass", f32, rows), _need(positions, "positions", i32, rows),
+               _need(history, "history", i32, 2 * B),
+               _need(w.block_table, "block_table", i32, B * p.max_blocks_per_seq),
+               _need(w.context_lens, "context_lens", i32, B), _need(w.k_pool, "k_pool"), _need(w.v_pool, "v_pool"),
+               _need(mass_out, "mass_out", f32, rows), _need(positions_out, "positions_out", i32, rows),
+               _need(history_out, "history_out", i32, 2 * B), _need(lens_out, "lens_out", i32, B),
+               _need(workspace, "workspace", "torch.uint8"), workspace.numel(), stream_handle(stream))

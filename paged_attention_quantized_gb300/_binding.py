@@ -56,6 +56,12 @@ class Fp4Problem(ctypes.Structure):
         "sf_interleaved", "num_sms", "grid_ctas")]
 
 
+class PromptProblem(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_int32) for k in (
+        "num_seqs", "total_q", "total_k", "num_q_heads", "num_kv_heads", "head_dim", "dtype", "out_dtype", "causal",
+        "q_stride", "k_stride", "v_stride")] + [("softmax_scale", ctypes.c_float)]
+
+
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"libpa.so is not built ({LIB_PATH}); run "
                       "`python -m paged_attention_quantized_gb300.build` (nvcc, sm_103a)")
@@ -92,6 +98,14 @@ _lib.pa_fp4_logits_workspace_size.restype = ctypes.c_int
 _lib.pa_fp4_logits_workspace_size.argtypes = [_P(Fp4Problem), _P(ctypes.c_size_t)]
 _lib.pa_fp4_logits.restype = ctypes.c_int
 _lib.pa_fp4_logits.argtypes = [_P(Fp4Problem)] + [_vp] * 7 + [ctypes.c_size_t, _vp, _vp]
+_lib.pa_prompt_attention.restype = ctypes.c_int
+_lib.pa_prompt_attention.argtypes = [_P(PromptProblem)] + [_vp] * 9
+_lib.pa_attention_mass.restype = ctypes.c_int
+_lib.pa_attention_mass.argtypes = [_P(Problem), ctypes.c_float] + [_vp] * 9
+_lib.pa_evict_workspace_size.restype = ctypes.c_int
+_lib.pa_evict_workspace_size.argtypes = [_P(Problem), ctypes.c_int32, _P(ctypes.c_size_t)]
+_lib.pa_evict.restype = ctypes.c_int
+_lib.pa_evict.argtypes = [_P(Problem)] + [ctypes.c_int32] * 3 + [_vp] * 12 + [ctypes.c_size_t, _vp]
 _lib.pa_get_error.restype = ctypes.c_int
 _lib.pa_get_error.argtypes = [_vp, _P(ctypes.c_uint32), _vp]
 
@@ -178,6 +192,31 @@ def pa_fp4_logits(p: Fp4Problem, q, sf_q, kv_fused, weights, context_lens, block
                   workspace_bytes, out, stream) -> None:
     _check(_lib.pa_fp4_logits(ctypes.byref(p), q, sf_q, kv_fused, weights, context_lens, block_table, workspace,
                               workspace_bytes, out, stream), "pa_fp4_logits")
+
+
+def pa_prompt_attention(p: PromptProblem, q, k, v, cu_q, cu_k, out, lse, dev_error, stream) -> None:
+    _check(_lib.pa_prompt_attention(ctypes.byref(p), q, k, v, cu_q, cu_k, out, lse, dev_error, stream),
+           "pa_prompt_attention")
+
+
+def pa_attention_mass(p: Problem, decay: float, q, k_pool, block_table, context_lens, k_scale, lse, mass, dev_error,
+                      stream) -> None:
+    _check(_lib.pa_attention_mass(ctypes.byref(p), decay, q, k_pool, block_table, context_lens, k_scale, lse, mass,
+                                  dev_error, stream), "pa_attention_mass")
+
+
+def pa_evict_workspace_size(p: Problem, budget: int) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib.pa_evict_workspace_size(ctypes.byref(p), int(budget), ctypes.byref(n)), "pa_evict_workspace_size")
+    return n.value
+
+
+def pa_evict(p: Problem, budget: int, sinks: int, recent: int, mass, positions, history, block_table, context_lens,
+             k_pool, v_pool, mass_out, positions_out, history_out, lens_out, workspace, workspace_bytes,
+             stream) -> None:
+    _check(_lib.pa_evict(ctypes.byref(p), budget, sinks, recent, mass, positions, history, block_table, context_lens,
+                         k_pool, v_pool, mass_out, positions_out, history_out, lens_out, workspace, workspace_bytes,
+                         stream), "pa_evict")
 
 
 def pa_get_error(workspace: int, stream) -> int:

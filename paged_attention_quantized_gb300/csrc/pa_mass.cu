@@ -1,0 +1,422 @@
+// Accumulated attention weight of the cached tokens:
+//
+//   mass[b][g][t] = decay mass[b][g][t]
+//                   + sum over query rows r of kv head g that see t of exp(c q_r . k_t - lse_r)
+//
+// The log-sum-exp is an input, so one pass over K suffices: a token's sum is
+// over rows, not over tokens, and no state is carried between tokens.  HBM
+// bound at decode: every K row is read once.
+//
+// Tokens are the M axis of mma.sync (S^T = K q^T): a warp holds 16 tokens of
+// one (request, kv head), the query rows are N, and a token's sum is a sum
+// over the accumulator's columns -- in registers, then across the four lanes
+// that share a token.  K goes straight from global memory into the operand
+// registers: lane i of a quad reads 16-byte pieces i, i + 4, ... of its two
+// rows, and the channel order this gives the contraction is applied to q as
+// well.  Units of 16 tokens in logical order (request, kv head, unit) are
+// shared evenly by persistent warps; each knows its share from a prefix sum
+// over context_lens that every CTA computes for itself.
+#include <algorithm>
+#include <cmath>
+
+#include "pa_attn.cuh"
+
+namespace pa {
+
+struct MassParams {
+    const uint8_t *q;
+    const uint8_t *k_pool;
+    const int32_t *block_table;
+    const int32_t *context_lens;
+    const float *k_scale;
+    const float *lse;
+    float *mass;
+    uint32_t *dev_error;
+    long long k_block;   // bytes per pool block
+    int k_codes;         // bytes of codes in a block (the per-token scales follow)
+    int B, n, Hq, Hkv, G, R, bs, tbl, max_ctx, num_blocks;
+    int q_dtype, k_mode, causal;
+    float decay, softmax_scale;
+};
+
+namespace mass {
+
+constexpr int THREADS = 256, UT = 16;  // tokens per unit
+constexpr int MAX_B = 8192;
+
+__device__ __forceinline__ float q_val(const uint8_t *row, int ch, int dtype) {
+    const uint16_t u = reinterpret_cast<const uint16_t *>(row)[ch];
+    return dtype == PA_BF16 ? __uint_as_float((uint32_t)u << 16) : __half2float(__ushort_as_half(u));
+}
+
+// the channel of element e (0, 1) of operand word w (0 ..) of 16-byte piece
+// `piece` of a row of BITS-bit codes
+template <int BITS>
+__device__ __forceinline__ int channel_of(int piece, int w, int e) {
+    if (BITS == 16) return piece * 8 + 2 * w + e;
+    if (BITS == 8) return piece * 16 + 2 * w + e;
+    return piece * 32 + 8 * (w >> 2) + (w & 3) + 4 * e;  // nibbles k and k + 4 of a 32-bit word
+}
+
+// one 16-byte piece of codes -> its operand words (f16x2 or bf16x2)
+template <int KV>
+__device__ __forceinline__ void decode(uint4 v, uint32_t *w) {
+    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (KV == PA_F16 || KV == PA_BF16) {
+            w[i] = in[i];
+        } else if constexpr (KV == PA_E4M3) {
+            w[2 * i] = e4m3x2_f16x2(in[i]);
+            w[2 * i + 1] = e4m3x2_f16x2(in[i] >> 16);
+        } else if constexpr (KV == PA_INT8) {
+            const uint32_t u = in[i] ^ 0x80808080u;
+            w[2 * i] = u8pair_f16x2(u, 0x4140);
+            w[2 * i + 1] = u8pair_f16x2(u, 0x4342);
+        } else {
+            w[4 * i] = s4lo_f16x2(in[i]);
+            w[4 * i + 1] = s4hi_f16x2(in[i]);
+            w[4 * i + 2] = s4lo_f16x2(in[i] >> 8);
+            w[4 * i + 3] = s4hi_f16x2(in[i] >> 8);
+        }
+    }
+}
+
+// NB blocks of 8 query rows at a time; NT terms per query value
+template <int D, int KV, int NB, int NT>
+__global__ void __launch_bounds__(THREADS) pa_mass_kernel(MassParams P) {
+    constexpr int BITS = KV == PA_INT4 ? 4 : (KV == PA_E4M3 || KV == PA_INT8) ? 8 : 16;
+    constexpr bool BF = KV == PA_BF16;
+    constexpr int PIECES = D * BITS / 8 / 64;     // 16-byte pieces per lane and row
+    constexpr int WORDS = 64 / BITS;              // operand words per piece
+    constexpr int QW = PIECES * WORDS;            // operand words per lane and query row
+    extern __shared__ int ps[];                   // units before request b (B + 1 entries)
+    __shared__ int warp_tot[THREADS / 32];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const float NaN = __int_as_float(0x7fc00000);
+
+    // ---- prefix sum of the requests' units
+    int carry = 0;
+    bool bad_len = false;
+    for (int base = 0; base < P.B; base += THREADS) {
+        const int b = base + tid;
+        int u = 0;
+        if (b < P.B) {
+            const int L = P.context_lens[b];
+            if (L < 0 || L > P.max_ctx || (long long)L > (long long)P.tbl * P.bs) bad_len = true;
+            else u = (L + UT - 1) / UT;
+        }
+        int x = u;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        if (lane == 31) warp_tot[warp] = x;
+        __syncthreads();
+        int before = carry, all = 0;
+#pragma unroll
+        for (int i = 0; i < THREADS / 32; ++i) {
+            const int t = warp_tot[i];
+            if (i < warp) before += t;
+            all += t;
+        }
+        if (b < P.B) ps[b] = before + x - u;
+        carry += all;
+        __syncthreads();
+    }
+    if (tid == 0) ps[P.B] = carry;
+    if (bad_len && blockIdx.x == 0 && P.dev_error) atomicOr(P.dev_error, PA_DEV_ERR_CONTEXT_LEN);
+    __syncthreads();
+
+    const long long N = (long long)carry * P.Hkv;
+    const long long W = (long long)gridDim.x * (THREADS / 32), k = (long long)blockIdx.x * (THREADS / 32) + warp;
+    const long long x0 = k * N / W, x1 = (k + 1) * N / W;
+    if (x0 >= x1) return;
+    // the request of position x0: the last b with ps[b] * Hkv <= x0 and units of its own
+    int b;
+    {
+        const int u0 = (int)(x0 / P.Hkv);
+        int lo = 0, hi = P.B;  // ps[lo] <= u0 < ps[hi]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (ps[mid] <= u0) lo = mid;
+            else hi = mid;
+        }
+        b = lo;
+    }
+    long long rem = x0 - (long long)ps[b] * P.Hkv;
+    int units = ps[b + 1] - ps[b];
+    int g = (int)(rem / units), u = (int)(rem % units);
+
+    const int gr = lane >> 2, qi = lane & 3;
+    uint32_t qw[NB][NT][QW];
+    float sc[NB][2], ls[NB][2];
+    int vis[NB][2];
+    int L = P.context_lens[b];
+    bool fresh = true;
+
+    // operand words of query rows r0 .. r0 + 8 NB of (b, g), and the constants of
+    // the rows whose columns this lane's accumulators hold (2 qi, 2 qi + 1)
+    auto load_q = [&](int r0) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            const int r = r0 + nb * 8 + gr;
+            const bool ok = r < P.R;
+            const int j = ok ? r / P.G : 0, h = g * P.G + (ok ? r % P.G : 0);
+            const size_t row = ((size_t)b * P.n + j) * P.Hq + h;
+            const uint8_t *src = P.q + row * (2 * D);
+            const float *fold = P.k_mode == PA_SCALE_CHANNEL ? P.k_scale + (size_t)g * D : nullptr;
+            // f16 operands of other queries than plain f16 ones are scaled by a power of two into [-1, 1)
+            const bool scaled = !BF && (fold != nullptr || P.q_dtype == PA_BF16);
+            float mx = 0.f;
+            if (scaled) {
+#pragma unroll 1
+                for (int i = 0; i < QW; ++i)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int ch = channel_of<BITS>((i / WORDS) * 4 + qi, i % WORDS, e);
+                        const float v = ok ? q_val(src, ch, P.q_dtype) * (fold ? fold[ch] : 1.f) : 0.f;
+                        mx = fmaxf(mx, fabsf(v));
+                    }
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            }
+            int ex = 0;
+            if (mx > 0.f && mx < 3.0e38f) frexpf(mx, &ex);
+            ex = max(-120, min(120, ex));
+            const float up = __int_as_float((127 - ex) << 23), down = __int_as_float((127 + ex) << 23);
+#pragma unroll
+            for (int i = 0; i < QW; ++i) {
+                float v[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int ch = channel_of<BITS>((i / WORDS) * 4 + qi, i % WORDS, e);
+                    v[e] = ok ? q_val(src, ch, P.q_dtype) * (fold ? fold[ch] : 1.f) : 0.f;
+                    if (scaled) v[e] *= up;
+                }
+                const uint32_t hi = pack2<BF>(v[0], v[1]);
+                qw[nb][0][i] = hi;
+                if constexpr (NT == 2) {
+                    float a, c;
+                    if constexpr (BF) {
+                        a = __uint_as_float(hi << 16);
+                        c = __uint_as_float(hi & 0xFFFF0000u);
+                    } else {
+                        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+                        a = f.x;
+                        c = f.y;
+                    }
+                    qw[nb][1][i] = pack2<BF>(v[0] - a, v[1] - c);
+                }
+            }
+            const float ks = P.k_mode == PA_SCALE_TENSOR ? P.k_scale[0] : 1.f;
+            const float mysc = P.softmax_scale * ks * down;
+            const float myls = ok ? P.lse[row] : 0.f;
+            const int myvis = (!ok || myls == -INFINITY) ? 0 : P.causal ? L - (P.n - 1 - j) : L;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int from = (2 * qi + e) * 4;
+                sc[nb][e] = __shfl_sync(0xffffffffu, mysc, from);
+                ls[nb][e] = __shfl_sync(0xffffffffu, myls, from);
+                vis[nb][e] = __shfl_sync(0xffffffffu, myvis, from);
+            }
+        }
+    };
+
+    uint32_t err = 0;
+    for (long long x = x0; x < x1; ++x) {
+        const int t0 = u * UT;
+        const int blk = P.block_table[(size_t)b * P.tbl + t0 / P.bs];
+        const bool okb = blk >= 1 && blk < P.num_blocks;
+        const int slot = t0 % P.bs;
+        uint4 raw[2][PIECES];
+        float ts[2] = {1.f, 1.f}, old[1];
+        const int tok[2] = {t0 + gr, t0 + gr + 8};
+        const uint8_t *base = P.k_pool + (size_t)(okb ? blk : 0) * P.k_block;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const uint4 *src = reinterpret_cast<const uint4 *>(base + ((size_t)g * P.bs + slot + gr + 8 * e) * (D * BITS / 8));
+            const bool live = okb && tok[e] < L;
+#pragma unroll
+            for (int c = 0; c < PIECES; ++c)
+                raw[e][c] = live ? __ldg(src + 4 * c + qi) : make_uint4(0u, 0u, 0u, 0u);
+            if (KV == PA_E4M3 && P.k_mode == PA_SCALE_TOKEN && live)
+                ts[e] = __ldg(reinterpret_cast<const float *>(base + P.k_codes) + (size_t)g * P.bs + slot + gr + 8 * e);
+        }
+        // lane 0 of a quad writes token gr, lane 1 token gr + 8
+        const int mytok = t0 + gr + 8 * qi;
+        float *out = P.mass + ((size_t)b * P.Hkv + g) * P.max_ctx + mytok;
+        const bool writes = qi < 2 && mytok < L;
+        old[0] = writes && P.decay != 0.f ? *out : 0.f;
+
+        float tot[2] = {0.f, 0.f};
+        for (int r0 = 0; r0 < P.R; r0 += 8 * NB) {
+            if (fresh || P.R > 8 * NB) load_q(r0);
+            fresh = false;
+            float acc[NB][NT][4];
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[nb][t][e] = 0.f;
+#pragma unroll
+            for (int c = 0; c < PIECES; ++c) {
+                uint32_t w0[WORDS], w1[WORDS];
+                decode<KV>(raw[0][c], w0);
+                decode<KV>(raw[1][c], w1);
+#pragma unroll
+                for (int s = 0; s < WORDS / 2; ++s) {
+                    const uint32_t a[4] = {w0[2 * s], w1[2 * s], w0[2 * s + 1], w1[2 * s + 1]};
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+                            mma16816<BF>(acc[nb][t], a, qw[nb][t][c * WORDS + 2 * s], qw[nb][t][c * WORDS + 2 * s + 1]);
+                }
+            }
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float z = NT == 2 ? acc[nb][0][e] + acc[nb][NT - 1][e] : acc[nb][0][e];
+                    const float d = fmaf(z * ts[e >> 1], sc[nb][e & 1], -ls[nb][e & 1]);
+                    const float p = ex2(d * LOG2E);
+                    tot[e >> 1] += tok[e >> 1] < vis[nb][e & 1] ? p : 0.f;
+                }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            tot[e] += __shfl_xor_sync(0xffffffffu, tot[e], 1);
+            tot[e] += __shfl_xor_sync(0xffffffffu, tot[e], 2);
+        }
+        if (!okb) err |= PA_DEV_ERR_BLOCK_ID;
+        if (writes) {
+            const float got = qi == 0 ? tot[0] : tot[1];
+            *out = !okb ? NaN : P.decay != 0.f ? fmaf(P.decay, old[0], got) : got;
+        }
+        // next unit in logical order
+        if (++u == units) {
+            u = 0;
+            fresh = true;
+            if (++g == P.Hkv) {
+                g = 0;
+                do ++b;
+                while (b < P.B && ps[b + 1] == ps[b]);
+                if (b >= P.B) break;
+                units = ps[b + 1] - ps[b];
+                L = P.context_lens[b];
+            }
+        }
+    }
+    if (err && lane == 0 && P.dev_error) atomicOr(P.dev_error, err);
+}
+
+template <int D, int KV, int NT>
+cudaError_t launch(const MassParams &P, int sms, cudaStream_t s) {
+    const size_t smem = ((size_t)P.B + 1) * 4;
+    auto go = [&](auto kernel) -> cudaError_t {
+        int per = 0;
+        cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, THREADS, smem);
+        if (e != cudaSuccess) return e;
+        kernel<<<sms * std::max(1, per), THREADS, smem, s>>>(P);
+        return cudaPeekAtLastError();
+    };
+    return P.R <= 8 ? go(pa_mass_kernel<D, KV, 1, NT>) : go(pa_mass_kernel<D, KV, 2, NT>);
+}
+
+template <int D>
+cudaError_t dispatch(const MassParams &P, int kv, int sms, cudaStream_t s) {
+    const bool fold = P.k_mode == PA_SCALE_CHANNEL;
+    switch (kv) {
+        case PA_F16: return launch<D, PA_F16, 1>(P, sms, s);
+        case PA_BF16:  // f16 queries have 11 bits: two bf16 terms hold them
+            return P.q_dtype == PA_BF16 ? launch<D, PA_BF16, 1>(P, sms, s) : launch<D, PA_BF16, 2>(P, sms, s);
+        case PA_E4M3: return fold ? launch<D, PA_E4M3, 2>(P, sms, s) : launch<D, PA_E4M3, 1>(P, sms, s);
+        case PA_INT8: return fold ? launch<D, PA_INT8, 2>(P, sms, s) : launch<D, PA_INT8, 1>(P, sms, s);
+        case PA_INT4:
+            if constexpr (D >= 128) return fold ? launch<D, PA_INT4, 2>(P, sms, s) : launch<D, PA_INT4, 1>(P, sms, s);
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace mass
+}  // namespace pa
+
+extern "C" PA_API pa_status pa_attention_mass(const pa_problem *p, float decay, const void *q, const void *k_pool,
+                                              const int32_t *block_table, const int32_t *context_lens,
+                                              const float *k_scale, const float *lse, float *mass, uint32_t *dev_error,
+                                              pa_stream_t stream) {
+    if (p == nullptr) return PA_ERR_INVALID_ARG;
+    if (p->batch < 0 || p->next_n < 1 || p->num_q_heads < 1 || p->num_kv_heads < 1 ||
+        p->num_q_heads % p->num_kv_heads != 0 || p->head_dim_k < 1 || p->block_size < 1 || p->num_blocks < 1 ||
+        p->max_blocks_per_seq < 1 || p->max_context_len < 0 || p->num_sms < 0)
+        return PA_ERR_INVALID_ARG;
+    if ((p->q_dtype != PA_F16 && p->q_dtype != PA_BF16) || p->kv_dtype < PA_F16 || p->kv_dtype > PA_INT4 ||
+        p->k_scale_mode < PA_SCALE_NONE || p->k_scale_mode > PA_SCALE_TOKEN || (p->causal != 0 && p->causal != 1) ||
+        !std::isfinite(p->softmax_scale) || !std::isfinite(decay))
+        return PA_ERR_INVALID_ARG;
+    const int D = p->head_dim_k, kv = p->kv_dtype;
+    if ((D != 64 && D != 128 && D != 256) || (kv == PA_INT4 && D == 64) || p->block_size % 16 != 0 ||
+        p->batch > pa::mass::MAX_B)
+        return PA_ERR_UNSUPPORTED;
+    const bool half = kv == PA_F16 || kv == PA_BF16;
+    if ((half && p->k_scale_mode > PA_SCALE_TENSOR) || (kv != PA_E4M3 && p->k_scale_mode == PA_SCALE_TOKEN))
+        return PA_ERR_UNSUPPORTED;
+    const int G = p->num_q_heads / p->num_kv_heads;
+    const long long R = (long long)G * p->next_n;
+    const int bits = half ? 16 : kv == PA_INT4 ? 4 : 8;
+    const long long codes = (long long)p->num_kv_heads * p->block_size * (D * bits / 8);
+    // units of 16 tokens are counted in 32 bits, over the batch
+    if (R > (1 << 20) || codes > 0x7FFFFFFFll ||
+        (long long)p->batch * (p->max_context_len / 16 + 1) > 0x7FFFFFFFll)
+        return PA_ERR_UNSUPPORTED;
+    if (p->batch == 0 || p->max_context_len == 0) return PA_OK;
+    if (q == nullptr || k_pool == nullptr || block_table == nullptr || context_lens == nullptr || lse == nullptr ||
+        mass == nullptr ||
+        ((p->k_scale_mode == PA_SCALE_TENSOR || p->k_scale_mode == PA_SCALE_CHANNEL) && k_scale == nullptr))
+        return PA_ERR_INVALID_ARG;
+    auto off = [](const void *x, uintptr_t a) { return (reinterpret_cast<uintptr_t>(x) & (a - 1)) != 0; };
+    if (off(q, 16) || off(k_pool, 16) || off(block_table, 4) || off(context_lens, 4) || off(lse, 4) || off(mass, 4) ||
+        off(k_scale, 4) || off(dev_error, 4))
+        return PA_ERR_INVALID_ARG;
+    int sms = p->num_sms;
+    if (sms == 0) {
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+            return PA_ERR_CUDA;
+    }
+    pa::MassParams P;
+    P.q = static_cast<const uint8_t *>(q);
+    P.k_pool = static_cast<const uint8_t *>(k_pool);
+    P.block_table = block_table;
+    P.context_lens = context_lens;
+    P.k_scale = k_scale;
+    P.lse = lse;
+    P.mass = mass;
+    P.dev_error = dev_error;
+    P.k_block = codes + (p->k_scale_mode == PA_SCALE_TOKEN ? (long long)p->num_kv_heads * p->block_size * 4 : 0);
+    P.k_codes = (int)codes;
+    P.B = p->batch;
+    P.n = p->next_n;
+    P.Hq = p->num_q_heads;
+    P.Hkv = p->num_kv_heads;
+    P.G = G;
+    P.R = (int)R;
+    P.bs = p->block_size;
+    P.tbl = p->max_blocks_per_seq;
+    P.max_ctx = p->max_context_len;
+    P.num_blocks = p->num_blocks;
+    P.q_dtype = p->q_dtype;
+    P.k_mode = p->k_scale_mode;
+    P.causal = p->causal;
+    P.decay = decay;
+    P.softmax_scale = p->softmax_scale;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const cudaError_t e = D == 64    ? pa::mass::dispatch<64>(P, kv, sms, s)
+                          : D == 128 ? pa::mass::dispatch<128>(P, kv, sms, s)
+                                     : pa::mass::dispatch<256>(P, kv, sms, s);
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
