@@ -535,7 +535,7 @@ PA_API pa_status pa_prompt_attention(const pa_prompt_problem *p, const void *q, 
  * Supported: head_dim_k 64, 128 or 256 (INT4: 128 or 256), block_size a
  * multiple of 16; f16 / bf16 codes with no or one scale, E4M3 with any scale
  * mode (TOKEN: the scales in the blocks), INT8 / INT4 with no, one or
- * per-channel scales; batch <= 8192; other problems return
+ * per-channel scales; batch <= 4096; other problems return
  * PA_ERR_UNSUPPORTED.  A request whose length breaks the contract
  * (PA_DEV_ERR_CONTEXT_LEN) is left as it is; tokens of a block whose id is
  * outside [1, num_blocks) get NaN (PA_DEV_ERR_BLOCK_ID).  One kernel launch;

@@ -19,70 +19,14 @@
 #include <algorithm>
 #include <cmath>
 
-#include "pa_attn.cuh"
+#include "pa_mass.cuh"
 
 namespace pa {
-
-struct MassParams {
-    const uint8_t *q;
-    const uint8_t *k_pool;
-    const int32_t *block_table;
-    const int32_t *context_lens;
-    const float *k_scale;
-    const float *lse;
-    float *mass;
-    uint32_t *dev_error;
-    long long k_block;   // bytes per pool block
-    int k_codes;         // bytes of codes in a block (the per-token scales follow)
-    int B, n, Hq, Hkv, G, R, bs, tbl, max_ctx, num_blocks;
-    int q_dtype, k_mode, causal;
-    float decay, softmax_scale;
-};
-
 namespace mass {
 
 constexpr int THREADS = 256, UT = 16;  // tokens per unit
-constexpr int MAX_B = 8192;
 
-__device__ __forceinline__ float q_val(const uint8_t *row, int ch, int dtype) {
-    const uint16_t u = reinterpret_cast<const uint16_t *>(row)[ch];
-    return dtype == PA_BF16 ? __uint_as_float((uint32_t)u << 16) : __half2float(__ushort_as_half(u));
-}
-
-// the channel of element e (0, 1) of operand word w (0 ..) of 16-byte piece
-// `piece` of a row of BITS-bit codes
-template <int BITS>
-__device__ __forceinline__ int channel_of(int piece, int w, int e) {
-    if (BITS == 16) return piece * 8 + 2 * w + e;
-    if (BITS == 8) return piece * 16 + 2 * w + e;
-    return piece * 32 + 8 * (w >> 2) + (w & 3) + 4 * e;  // nibbles k and k + 4 of a 32-bit word
-}
-
-// one 16-byte piece of codes -> its operand words (f16x2 or bf16x2)
-template <int KV>
-__device__ __forceinline__ void decode(uint4 v, uint32_t *w) {
-    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if constexpr (KV == PA_F16 || KV == PA_BF16) {
-            w[i] = in[i];
-        } else if constexpr (KV == PA_E4M3) {
-            w[2 * i] = e4m3x2_f16x2(in[i]);
-            w[2 * i + 1] = e4m3x2_f16x2(in[i] >> 16);
-        } else if constexpr (KV == PA_INT8) {
-            const uint32_t u = in[i] ^ 0x80808080u;
-            w[2 * i] = u8pair_f16x2(u, 0x4140);
-            w[2 * i + 1] = u8pair_f16x2(u, 0x4342);
-        } else {
-            w[4 * i] = s4lo_f16x2(in[i]);
-            w[4 * i + 1] = s4hi_f16x2(in[i]);
-            w[4 * i + 2] = s4lo_f16x2(in[i] >> 8);
-            w[4 * i + 3] = s4hi_f16x2(in[i] >> 8);
-        }
-    }
-}
-
-// NB blocks of 8 query rows at a time; NT terms per query value
+// NB blocks of 8 query rows; NT terms per query value
 template <int D, int KV, int NB, int NT>
 __global__ void __launch_bounds__(THREADS) pa_mass_kernel(MassParams P) {
     constexpr int BITS = KV == PA_INT4 ? 4 : (KV == PA_E4M3 || KV == PA_INT8) ? 8 : 16;
@@ -95,56 +39,13 @@ __global__ void __launch_bounds__(THREADS) pa_mass_kernel(MassParams P) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const float NaN = __int_as_float(0x7fc00000);
 
-    // ---- prefix sum of the requests' units
-    int carry = 0;
-    bool bad_len = false;
-    for (int base = 0; base < P.B; base += THREADS) {
-        const int b = base + tid;
-        int u = 0;
-        if (b < P.B) {
-            const int L = P.context_lens[b];
-            if (L < 0 || L > P.max_ctx || (long long)L > (long long)P.tbl * P.bs) bad_len = true;
-            else u = (L + UT - 1) / UT;
-        }
-        int x = u;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
-        }
-        if (lane == 31) warp_tot[warp] = x;
-        __syncthreads();
-        int before = carry, all = 0;
-#pragma unroll
-        for (int i = 0; i < THREADS / 32; ++i) {
-            const int t = warp_tot[i];
-            if (i < warp) before += t;
-            all += t;
-        }
-        if (b < P.B) ps[b] = before + x - u;
-        carry += all;
-        __syncthreads();
-    }
-    if (tid == 0) ps[P.B] = carry;
+    const bool bad_len = scan_units<THREADS, UT>(P, ps, warp_tot);
     if (bad_len && blockIdx.x == 0 && P.dev_error) atomicOr(P.dev_error, PA_DEV_ERR_CONTEXT_LEN);
-    __syncthreads();
-
-    const long long N = (long long)carry * P.Hkv;
+    const long long N = (long long)ps[P.B] * P.Hkv;
     const long long W = (long long)gridDim.x * (THREADS / 32), k = (long long)blockIdx.x * (THREADS / 32) + warp;
     const long long x0 = k * N / W, x1 = (k + 1) * N / W;
     if (x0 >= x1) return;
-    // the request of position x0: the last b with ps[b] * Hkv <= x0 and units of its own
-    int b;
-    {
-        const int u0 = (int)(x0 / P.Hkv);
-        int lo = 0, hi = P.B;  // ps[lo] <= u0 < ps[hi]
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (ps[mid] <= u0) lo = mid;
-            else hi = mid;
-        }
-        b = lo;
-    }
+    int b = request_of(ps, P.B, (int)(x0 / P.Hkv));
     long long rem = x0 - (long long)ps[b] * P.Hkv;
     int units = ps[b + 1] - ps[b];
     int g = (int)(rem / units), u = (int)(rem % units);
@@ -156,12 +57,12 @@ __global__ void __launch_bounds__(THREADS) pa_mass_kernel(MassParams P) {
     int L = P.context_lens[b];
     bool fresh = true;
 
-    // operand words of query rows r0 .. r0 + 8 NB of (b, g), and the constants of
+    // operand words of the query rows of (b, g), and the constants of
     // the rows whose columns this lane's accumulators hold (2 qi, 2 qi + 1)
-    auto load_q = [&](int r0) {
+    auto load_q = [&]() {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-            const int r = r0 + nb * 8 + gr;
+            const int r = nb * 8 + gr;
             const bool ok = r < P.R;
             const int j = ok ? r / P.G : 0, h = g * P.G + (ok ? r % P.G : 0);
             const size_t row = ((size_t)b * P.n + j) * P.Hq + h;
@@ -251,8 +152,8 @@ __global__ void __launch_bounds__(THREADS) pa_mass_kernel(MassParams P) {
         old[0] = writes && P.decay != 0.f ? *out : 0.f;
 
         float tot[2] = {0.f, 0.f};
-        for (int r0 = 0; r0 < P.R; r0 += 8 * NB) {
-            if (fresh || P.R > 8 * NB) load_q(r0);
+        {
+            if (fresh) load_q();
             fresh = false;
             float acc[NB][NT][4];
 #pragma unroll
@@ -320,23 +221,31 @@ cudaError_t launch(const MassParams &P, int sms, cudaStream_t s) {
         int per = 0;
         cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, THREADS, smem);
         if (e != cudaSuccess) return e;
-        kernel<<<sms * std::max(1, per), THREADS, smem, s>>>(P);
+        // no warp without a unit of the longest possible batch
+        const long long units = (long long)P.B * P.Hkv * ((P.max_ctx + UT - 1) / UT);
+        const long long ctas = std::min<long long>((long long)sms * std::max(1, per), (units + THREADS / 32 - 1) / (THREADS / 32));
+        kernel<<<(unsigned)ctas, THREADS, smem, s>>>(P);
         return cudaPeekAtLastError();
     };
     return P.R <= 8 ? go(pa_mass_kernel<D, KV, 1, NT>) : go(pa_mass_kernel<D, KV, 2, NT>);
 }
 
+// query terms: a folded per-channel scale, and f16 queries (11 bits) against
+// bf16 operands, need two
+int query_terms(const MassParams &P, int kv) {
+    return (P.k_mode == PA_SCALE_CHANNEL || (kv == PA_BF16 && P.q_dtype == PA_F16)) ? 2 : 1;
+}
+
 template <int D>
 cudaError_t dispatch(const MassParams &P, int kv, int sms, cudaStream_t s) {
-    const bool fold = P.k_mode == PA_SCALE_CHANNEL;
+    const bool two = query_terms(P, kv) == 2;
     switch (kv) {
         case PA_F16: return launch<D, PA_F16, 1>(P, sms, s);
-        case PA_BF16:  // f16 queries have 11 bits: two bf16 terms hold them
-            return P.q_dtype == PA_BF16 ? launch<D, PA_BF16, 1>(P, sms, s) : launch<D, PA_BF16, 2>(P, sms, s);
-        case PA_E4M3: return fold ? launch<D, PA_E4M3, 2>(P, sms, s) : launch<D, PA_E4M3, 1>(P, sms, s);
-        case PA_INT8: return fold ? launch<D, PA_INT8, 2>(P, sms, s) : launch<D, PA_INT8, 1>(P, sms, s);
+        case PA_BF16: return two ? launch<D, PA_BF16, 2>(P, sms, s) : launch<D, PA_BF16, 1>(P, sms, s);
+        case PA_E4M3: return two ? launch<D, PA_E4M3, 2>(P, sms, s) : launch<D, PA_E4M3, 1>(P, sms, s);
+        case PA_INT8: return two ? launch<D, PA_INT8, 2>(P, sms, s) : launch<D, PA_INT8, 1>(P, sms, s);
         case PA_INT4:
-            if constexpr (D >= 128) return fold ? launch<D, PA_INT4, 2>(P, sms, s) : launch<D, PA_INT4, 1>(P, sms, s);
+            if constexpr (D >= 128) return two ? launch<D, PA_INT4, 2>(P, sms, s) : launch<D, PA_INT4, 1>(P, sms, s);
     }
     return cudaErrorInvalidValue;
 }
@@ -415,7 +324,8 @@ extern "C" PA_API pa_status pa_attention_mass(const pa_problem *p, float decay, 
     P.decay = decay;
     P.softmax_scale = p->softmax_scale;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = D == 64    ? pa::mass::dispatch<64>(P, kv, sms, s)
+    const cudaError_t e = P.R > 16   ? pa::mass::launch_mass_tc(P, kv, D, pa::mass::query_terms(P, kv), sms, s)
+                          : D == 64  ? pa::mass::dispatch<64>(P, kv, sms, s)
                           : D == 128 ? pa::mass::dispatch<128>(P, kv, sms, s)
                                      : pa::mass::dispatch<256>(P, kv, sms, s);
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
