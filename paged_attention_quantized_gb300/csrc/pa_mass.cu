@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(THREADS) pa_mass_kernel(MassParams P) {
     uint32_t err = 0;
     for (long long x = x0; x < x1; ++x) {
         const int t0 = u * UT;
-        const int blk = P.block_table[(size_t)b * P.tbl + t0 / P.bs];
+        const int blk = P.block_table[(size_t)b * P.tbl + __umulhi((unsigned)t0, P.bs_mul)];
         const bool okb = blk >= 1 && blk < P.num_blocks;
         const int slot = t0 % P.bs;
         uint4 raw[2][PIECES];
@@ -279,6 +279,7 @@ extern "C" PA_API pa_status pa_attention_mass(const pa_problem *p, float decay, 
     const long long codes = (long long)p->num_kv_heads * p->block_size * (D * bits / 8);
     // units of 16 tokens are counted in 32 bits, over the batch
     if (R > (1 << 20) || codes > 0x7FFFFFFFll ||
+        ((long long)p->max_context_len + 128) * p->block_size >= (1ll << 32) ||
         (long long)p->batch * (p->max_context_len / 16 + 1) > 0x7FFFFFFFll)
         return PA_ERR_UNSUPPORTED;
     if (p->batch == 0 || p->max_context_len == 0) return PA_OK;
@@ -321,6 +322,7 @@ extern "C" PA_API pa_status pa_attention_mass(const pa_problem *p, float decay, 
     P.q_dtype = p->q_dtype;
     P.k_mode = p->k_scale_mode;
     P.causal = p->causal;
+    P.bs_mul = (unsigned)((1ull << 32) / (unsigned)p->block_size) + 1u;
     P.decay = decay;
     P.softmax_scale = p->softmax_scale;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -20,6 +20,7 @@ struct MassParams {
     int k_codes;         // bytes of codes in a block (the per-token scales follow)
     int B, n, Hq, Hkv, G, R, bs, tbl, max_ctx, num_blocks;
     int q_dtype, k_mode, causal;
+    unsigned bs_mul;     // floor(2^32 / bs) + 1: token / bs is the high word of the product (tokens * bs < 2^32)
     float decay, softmax_scale;
 };
 

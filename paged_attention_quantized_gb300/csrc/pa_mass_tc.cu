@@ -11,16 +11,17 @@
 // it, and the sum over rows needs no shuffles: in tensor memory a token is a
 // lane, so one thread adds up its token's rows.
 //
-// Roles (17 warps): two loader warpgroups take alternate tiles -- 16-bit codes
-// are copied asynchronously into the swizzled operand layout, quantized ones
-// loaded a tile ahead into registers, decoded exactly and stored there; one
-// warp issues the MMAs; two epilogue warpgroups, one per S^T buffer, sum and
+// Roles (17 warps at work): two loader warpgroups take alternate tiles -- 16-bit
+// codes are copied asynchronously into the swizzled operand layout, quantized
+// ones loaded a tile ahead into registers, decoded exactly and stored there;
+// one warp issues the MMAs; two epilogue warpgroups, one per S^T buffer, sum and
 // update the total (a tile always falls to the same warpgroup, so the passes
 // over chunks of rows are ordered) and stage the query rows of each segment.
 // Tiles in logical order (request, kv head, tile) are shared evenly by
 // persistent CTAs.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "pa_mass.cuh"
 #include "pa_tc.cuh"
@@ -33,7 +34,10 @@ namespace mtc {
 using namespace tc;
 
 constexpr int CH = 128;                                   // tokens per tile
-constexpr int W_EPI = 8, W_MMA = 16, THREADS = 17 * 32;  // warps 0-7 load
+constexpr int W_EPI = 8, W_MMA = 16;   // warps 0-7 load, 8-15 sum, 16 issues (17-19 idle: their registers go to the others)
+constexpr int THREADS = 640;
+constexpr int REGS_LAUNCH = 96, REGS_WORK = 104, REGS_MMA = 64;
+static_assert(512 * REGS_WORK + 128 * REGS_MMA <= THREADS * REGS_LAUNCH, "register split exceeds the launch");
 
 template <int D>
 struct Lay {
@@ -99,6 +103,29 @@ __device__ __forceinline__ uint32_t op_off(int rows, int t, int c) {
     return (uint32_t)((c >> 3) * rows * 128 + t * 128 + (((c & 7) ^ (t & 7)) << 4));
 }
 
+// the sum over rows of a tile that some row does not see all of (the last
+// ones of a request): rows taken two by two, each against its visible length
+__device__ __noinline__ float masked_sum(uint32_t tl, int rp, int nt, const float *cst, const int *vs, int tok,
+                                         float ts) {
+    float tot = 0.f;
+#pragma unroll 1
+    for (int r0 = 0; r0 < rp; r0 += 8) {
+        uint32_t z[8], z2[8];
+        tmem_ld8_nowait(tl + (uint32_t)r0, z);
+        if (nt == 2) tmem_ld8_nowait(tl + (uint32_t)(rp + r0), z2);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float d = __uint_as_float(z[e]);
+            if (nt == 2) d += __uint_as_float(z2[e]);
+            const int r = r0 + e;
+            d = fmaf(d * ts, cst[(r >> 1) * 4 + (r & 1)], cst[(r >> 1) * 4 + 2 + (r & 1)]);
+            if (tok < vs[r]) tot += ex2(d * LOG2E);
+        }
+    }
+    return tot;
+}
+
 }  // namespace mtc
 
 template <int D, int KV>
@@ -155,85 +182,99 @@ __global__ void __launch_bounds__(mtc::THREADS, 1) pa_mass_tc_kernel(MassParams 
     walk_piece(w, P, ps);
 
     if (warp < W_EPI) {
+        regs_inc<REGS_WORK>();
         // ================================================== loaders: tile i by warpgroup i & 1
         const int wg = warp >> 2, wq = warp & 3;  // the warp's 32 tokens: 32 wq ..
-        int i = 0;
-        auto skip = [&](int k) {
-            for (int q = 0; q < k && !w.end; ++q) {
-                walk_next(w, P, ps, chunks);
-                ++i;
-            }
+        int i = wg;                               // the next tile to publish
+        // The warp's 32 tokens are two runs of 16 rows, each contiguous in its
+        // block.  Their places are known QD tiles of this warpgroup ahead, so that
+        // the block ids have arrived when the rows are asked for.
+        struct Place {
+            int id[2], off[2], left;  // blocks, byte offsets in them, tokens of the 32 that exist
         };
-        auto ids_of = [&](const Walk &v, int *id) {  // blocks of the warp's two halves of 16 tokens
+        constexpr int QD = 3;
+        Place pl[QD];
+        auto step = [&]() {
+            if (!w.end) walk_next(w, P, ps, chunks);
+        };
+        auto place = [&](Place &q) {
+            q.left = w.end ? 0 : w.L - (w.u * CH + 32 * wq);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int t = v.u * CH + 32 * wq + 16 * h;
-                id[h] = (!v.end && t < v.L) ? P.block_table[(size_t)v.b * P.tbl + t / P.bs] : 0;
+                const int t = w.u * CH + 32 * wq + 16 * h;
+                const int col = (int)__umulhi((unsigned)t, P.bs_mul);
+                q.id[h] = (!w.end && t < w.L) ? P.block_table[(size_t)w.b * P.tbl + col] : 0;
+                q.off[h] = (w.g * P.bs + t - col * P.bs) * RB;
             }
+            step();
+            step();
         };
-        // global address of piece k (of PR) of this lane, and whether it is a token's
-        auto piece = [&](const Walk &v, const int *id, int k, bool &live) -> const uint8_t * {
-            const int q = k * 32 + lane, t = 32 * wq + q / PR;
-            const int blk = k < PR / 2 ? id[0] : id[1];
-            live = !v.end && v.u * CH + t < v.L && blk >= 1 && blk < P.num_blocks;
-            return P.k_pool + (size_t)(live ? blk : 0) * P.k_block +
-                   ((size_t)v.g * P.bs + (v.u * CH + t) % P.bs) * RB + (q % PR) * 16;
+        if (wg == 1) step();
+#pragma unroll
+        for (int q = 0; q < QD; ++q) place(pl[q]);
+        auto rotate = [&]() {
+#pragma unroll
+            for (int q = 0; q + 1 < QD; ++q) pl[q] = pl[q + 1];
+            place(pl[QD - 1]);
         };
-        skip(wg);
+        const int mine = (int)(x1 - x0) * chunks;  // tiles of the CTA, all passes
+        const uint8_t *run[2];
+        auto runs_of = [&](const Place &q) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                run[h] = q.id[h] >= 1 && q.id[h] < P.num_blocks ? P.k_pool + (size_t)q.id[h] * P.k_block + q.off[h]
+                                                               : nullptr;
+        };
+        // piece k (of PR) of this lane lies in run k / (PR / 2)
+        auto piece = [&](int k, int left, bool &live) -> const uint8_t * {
+            const int h = k < PR / 2 ? 0 : 1, q = k * 32 + lane;
+            live = run[h] != nullptr && q / PR < left;
+            return live ? run[h] + (q - h * 16 * PR) * 16 : P.k_pool;
+        };
         if constexpr (BITS == 16) {
-            int id[2], issued = 0, done = 0;
-            Walk ahead = w;
-            ids_of(ahead, id);
-            // keep up to PF tiles of this warpgroup in flight, then publish the oldest
+            // up to PF tiles of this warpgroup in flight, then publish the oldest
             constexpr int PF = NA > 2 ? 2 : 1;
-            int ai = i;
-            bool ok = true;
-            while (ok && (done < issued || !ahead.end)) {
-                if (!ahead.end && issued - done < PF) {
+            int ai = wg;  // the next tile to copy
+            while (i < mine) {
+                if (ai < mine && ai - i < 2 * PF) {
                     const int slot = ai % NA;
-                    if (ai >= NA && !warp_wait(&bars[Y::B_AFREE + slot], (ai / NA - 1) & 1, abort, err)) {
-                        ok = false;
-                        break;
-                    }
+                    if (ai >= NA && !warp_wait(&bars[Y::B_AFREE + slot], (ai / NA - 1) & 1, abort, err)) break;
                     const uint32_t dst = sb + Y::A_OFF + slot * Y::A_BYTES;
+                    const int left = pl[0].left;
+                    runs_of(pl[0]);
 #pragma unroll 4
                     for (int k = 0; k < PR; ++k) {
                         bool live;
-                        const uint8_t *src = piece(ahead, id, k, live);
+                        const uint8_t *src = piece(k, left, live);
                         const int q = k * 32 + lane;
                         cp_async16(dst + op_off(CH, 32 * wq + q / PR, q % PR), src, live);
                     }
                     asm volatile("cp.async.commit_group;" ::: "memory");
-                    ++issued;
-                    for (int q = 0; q < 2 && !ahead.end; ++q) walk_next(ahead, P, ps, chunks);
                     ai += 2;
-                    ids_of(ahead, id);
-                    if (!ahead.end && issued - done < PF) continue;
+                    rotate();
+                    if (ai < mine && ai - i < 2 * PF) continue;
                 }
-                if (issued - done > 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+                if (ai - i > 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
                 else asm volatile("cp.async.wait_group 0;" ::: "memory");
                 fence_proxy_async_smem();
-                warp_arrive(&bars[Y::B_AFULL + (i + 2 * done) % NA]);
-                ++done;
+                warp_arrive(&bars[Y::B_AFULL + i % NA]);
+                i += 2;
             }
             asm volatile("cp.async.wait_group 0;" ::: "memory");
         } else {
-            int id[2], id2[2];
-            ids_of(w, id);
             uint4 raw[PR];
             auto fetch = [&]() {
+                const int left = pl[0].left;
+                runs_of(pl[0]);
 #pragma unroll
                 for (int k = 0; k < PR; ++k) {
                     bool live;
-                    const uint8_t *src = piece(w, id, k, live);
+                    const uint8_t *src = piece(k, left, live);
                     raw[k] = live ? __ldg(reinterpret_cast<const uint4 *>(src)) : make_uint4(0u, 0u, 0u, 0u);
                 }
             };
             fetch();
-            Walk v = w;
-            for (int q = 0; q < 2 && !v.end; ++q) walk_next(v, P, ps, chunks);
-            ids_of(v, id2);
-            while (!w.end) {
+            for (; i < mine; i += 2) {
                 const int slot = i % NA;
                 if (i >= NA && !warp_wait(&bars[Y::B_AFREE + slot], (i / NA - 1) & 1, abort, err)) break;
                 uint8_t *dst = smem + Y::A_OFF + slot * Y::A_BYTES;
@@ -248,34 +289,41 @@ __global__ void __launch_bounds__(mtc::THREADS, 1) pa_mass_tc_kernel(MassParams 
                         *reinterpret_cast<uint4 *>(dst + op_off(CH, t, c + o)) =
                             make_uint4(wd[4 * o], wd[4 * o + 1], wd[4 * o + 2], wd[4 * o + 3]);
                 }
-                // the next tile of this warpgroup: its blocks are known, load it now
-                w = v;
-                id[0] = id2[0];
-                id[1] = id2[1];
-                fetch();
                 fence_proxy_async_smem();
                 warp_arrive(&bars[Y::B_AFULL + slot]);
-                i += 2;
-                for (int q = 0; q < 2 && !v.end; ++q) walk_next(v, P, ps, chunks);
-                ids_of(v, id2);
+                rotate();
+                fetch();  // the next tile of this warpgroup, while this one is used
             }
         }
     } else if (warp < W_MMA) {
+        regs_inc<REGS_WORK>();
         // ================================================== sums over rows; query staging
         const int wg = (warp - W_EPI) >> 2, qd = warp & 3;
         const int t = 32 * qd + lane;
         const uint32_t tl = tmem + ((uint32_t)(32 * qd) << 16) + 256u * wg;
-        const int rp = (rows_c + 7) / 8 * 8;                    // rows of a term in the B operand
-        int seg = -1, pb = -1, pg = -1, pc = -1, sphase = 0, pua = -1;
+        const int rp = rows_c;  // rows of a term in the B operand
+        int seg = -1, sphase = 0;
         bool ok = true;
-        for (; !w.end && ok; walk_next(w, P, ps, chunks)) {
-            if (w.b != pb || w.g != pg || w.c != pc || w.ua != pua) {
-                // a new segment: its query rows, one warp per row
+        int f_blk = 0;
+        float f_old = 0.f;
+        const uint64_t l2e = f2(LOG2E, LOG2E);
+        for (; !w.end && ok; walk_piece(w, P, ps)) {
+            const int u1 = w.ua + ((w.ua ^ wg) & 1);  // this warpgroup's first tile of the piece
+            const int32_t *table = P.block_table + (size_t)w.b * P.tbl;
+            float *mass = P.mass + ((size_t)w.b * P.Hkv + w.g) * P.max_ctx;
+            for (w.c = 0; w.c < chunks && ok; ++w.c) {
+                const float dec = w.c == 0 ? P.decay : 1.f;
+                // the thread's token of tile u: its block and its total so far (of
+                // the passes before this one, which this thread wrote)
+                auto fetch_token = [&](int u) {
+                    const int tok = u * CH + t;
+                    const bool in = u < w.ue && tok < w.L;
+                    f_blk = in ? table[__umulhi((unsigned)tok, P.bs_mul)] : 0;
+                    f_old = in && dec != 0.f ? mass[tok] : 0.f;
+                };
+                fetch_token(u1);
+                // ---- a new segment: its query rows
                 ++seg;
-                pb = w.b;
-                pg = w.g;
-                pc = w.c;
-                pua = w.ua;
                 if (seg > 0 && !warp_wait(&bars[Y::B_QFREE], (seg - 1) & 1, abort, err)) {
                     ok = false;
                     break;
@@ -284,65 +332,106 @@ __global__ void __launch_bounds__(mtc::THREADS, 1) pa_mass_tc_kernel(MassParams 
                 int *vs = reinterpret_cast<int *>(smem + Y::VIS_OFF) + (seg & 1) * Y::NMAX;
                 const float *fold = P.k_mode == PA_SCALE_CHANNEL ? P.k_scale + (size_t)w.g * D : nullptr;
                 const bool scaled = !BF && (fold != nullptr || P.q_dtype == PA_BF16);
-                for (int rr = warp - W_EPI; rr < rp; rr += 8) {
-                    const int r = w.c * rows_c + rr;
-                    const bool rok = rr < rows_c && r < P.R;
-                    const int j = rok ? r / P.G : 0, h = w.g * P.G + (rok ? r % P.G : 0);
-                    const size_t row = ((size_t)w.b * P.n + j) * P.Hq + h;
-                    const uint8_t *src = P.q + row * (2 * D);
-                    // lane: operand words lane, lane + 32, ... (pairs of channels)
-                    float v[D / 64][2], mx = 0.f;
+                constexpr int WP = 64 / BITS;  // operand words per raw piece
+                float2 fv[D / 64];
 #pragma unroll
-                    for (int i = 0; i < D / 64; ++i)
+                for (int k = 0; k < D / 64; ++k) {
+                    const int pc = (lane + 32 * k) / WP, wd = (lane + 32 * k) % WP;
+                    fv[k] = fold ? make_float2(fold[channel_of<BITS>(pc, wd, 0)], fold[channel_of<BITS>(pc, wd, 1)])
+                                 : make_float2(1.f, 1.f);
+                }
+                // a warp takes QB rows at a time, all their loads in flight together
+                constexpr int QB = D == 256 ? 4 : 8;
+                for (int rr0 = (warp - W_EPI) * QB; rr0 < rp; rr0 += 8 * QB) {
+                    uint32_t raw[QB][D / 64];  // lane: operand words lane, lane + 32, ... (pairs of channels)
+                    float lse = -INFINITY;
+                    int vis = 0x7FFFFFFF;      // rows past R never count, and do not force the masked sum either
+                    int r = w.c * rows_c + rr0, j = r / P.G, hg = r - j * P.G;
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int word = lane + 32 * i;
-                            constexpr int WP = 64 / BITS;  // words per raw piece
-                            const int ch = channel_of<BITS>(word / WP, word % WP, e);
-                            v[i][e] = rok ? q_val(src, ch, P.q_dtype) * (fold ? fold[ch] : 1.f) : 0.f;
-                            mx = fmaxf(mx, fabsf(v[i][e]));
+                    for (int i = 0; i < QB; ++i, ++r) {
+                        const bool rok = rr0 + i < rows_c && r < P.R;
+                        const size_t row = ((size_t)w.b * P.n + j) * P.Hq + w.g * P.G + hg;
+                        const uint16_t *src = reinterpret_cast<const uint16_t *>(P.q + row * (2 * D));
+#pragma unroll
+                        for (int k = 0; k < D / 64; ++k) {
+                            if constexpr (BITS == 4) {
+                                const int c0 = channel_of<4>((lane + 32 * k) / WP, (lane + 32 * k) % WP, 0);
+                                raw[i][k] = rok ? (uint32_t)src[c0] | ((uint32_t)src[c0 + 4] << 16) : 0u;
+                            } else {
+                                raw[i][k] = rok ? reinterpret_cast<const uint32_t *>(src)[lane + 32 * k] : 0u;
+                            }
                         }
-                    float down = 1.f;
-                    if (scaled) {
-#pragma unroll
-                        for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                        int ex = 0;
-                        if (mx > 0.f && mx < 3.0e38f) frexpf(mx, &ex);
-                        ex = max(-120, min(120, ex));
-                        const float up = __int_as_float((127 - ex) << 23);
-                        down = __int_as_float((127 + ex) << 23);
-#pragma unroll
-                        for (int i = 0; i < D / 64; ++i) {
-                            v[i][0] *= up;
-                            v[i][1] *= up;
+                        if (lane == i && rok) {
+                            lse = P.lse[row];
+                            vis = P.causal ? w.L - (P.n - 1 - j) : w.L;
+                        }
+                        if (++hg == P.G) {
+                            hg = 0;
+                            ++j;
                         }
                     }
+                    auto pair = [&](int i, int k) -> float2 {
+                        const uint32_t x = raw[i][k];
+                        float2 f = P.q_dtype == PA_BF16
+                                       ? make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u))
+                                       : __half22float2(*reinterpret_cast<const __half2 *>(&x));
+                        f.x *= fv[k].x;
+                        f.y *= fv[k].y;
+                        return f;
+                    };
+                    float mx[QB], my_down = 1.f;
+                    if (scaled) {
 #pragma unroll
-                    for (int i = 0; i < D / 64; ++i) {
-                        const int word = lane + 32 * i, c = word >> 2;
-                        float a = v[i][0], d = v[i][1];
-                        for (int q = 0; q < nt; ++q) {
-                            const uint32_t x = pack2<BF>(a, d);
-                            *reinterpret_cast<uint32_t *>(smem + Y::Q_OFF + op_off(nt * rp, q * rp + rr, c) +
-                                                          4 * (word & 3)) = x;
-                            if constexpr (BF) {
-                                a -= __uint_as_float(x << 16);
-                                d -= __uint_as_float(x & 0xFFFF0000u);
-                            } else {
-                                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&x));
-                                a -= f.x;
-                                d -= f.y;
+                        for (int i = 0; i < QB; ++i) {
+                            mx[i] = 0.f;
+#pragma unroll
+                            for (int k = 0; k < D / 64; ++k) {
+                                const float2 f = pair(i, k);
+                                mx[i] = fmaxf(mx[i], fmaxf(fabsf(f.x), fabsf(f.y)));
+                            }
+                        }
+#pragma unroll
+                        for (int o = 16; o >= 1; o >>= 1)
+#pragma unroll
+                            for (int i = 0; i < QB; ++i) mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], o));
+                    }
+#pragma unroll
+                    for (int i = 0; i < QB; ++i) {
+                        float up = 1.f;
+                        if (scaled) {
+                            int ex = 0;
+                            if (mx[i] > 0.f && mx[i] < 3.0e38f) ex = (int)(__float_as_uint(mx[i]) >> 23) - 126;
+                            ex = max(-120, min(120, ex));
+                            up = __int_as_float((127 - ex) << 23);
+                            if (lane == i) my_down = __int_as_float((127 + ex) << 23);
+                        }
+#pragma unroll
+                        for (int k = 0; k < D / 64; ++k) {
+                            const int word = lane + 32 * k, c = word >> 2;
+                            const float2 f = pair(i, k);
+                            float a = f.x * up, d = f.y * up;
+                            for (int q = 0; q < nt; ++q) {
+                                const uint32_t x = pack2<BF>(a, d);
+                                *reinterpret_cast<uint32_t *>(smem + Y::Q_OFF + op_off(nt * rp, q * rp + rr0 + i, c) +
+                                                              4 * (word & 3)) = x;
+                                if constexpr (BF) {
+                                    a -= __uint_as_float(x << 16);
+                                    d -= __uint_as_float(x & 0xFFFF0000u);
+                                } else {
+                                    const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&x));
+                                    a -= h.x;
+                                    d -= h.y;
+                                }
                             }
                         }
                     }
-                    if (lane == 0) {
+                    if (lane < QB) {
+                        const int rr = rr0 + lane;
                         const float ks = P.k_mode == PA_SCALE_TENSOR ? P.k_scale[0] : 1.f;
-                        const float lse = rok ? P.lse[row] : -INFINITY;
-                        const bool on = rok && lse != -INFINITY;
-                        cst[(rr >> 1) * 4 + (rr & 1)] = on ? P.softmax_scale * ks * down : 0.f;
+                        const bool on = lse != -INFINITY;
+                        cst[(rr >> 1) * 4 + (rr & 1)] = on ? P.softmax_scale * ks * my_down : 0.f;
                         cst[(rr >> 1) * 4 + 2 + (rr & 1)] = on ? -lse : -INFINITY;
-                        // rows past R never count, and do not force the masked sum either
-                        vs[rr] = !rok ? 0x7FFFFFFF : !on ? 0 : P.causal ? w.L - (P.n - 1 - j) : w.L;
+                        vs[rr] = (vis != 0x7FFFFFFF && !on) ? 0 : vis;
                     }
                 }
                 fence_proxy_async_smem();
@@ -351,79 +440,96 @@ __global__ void __launch_bounds__(mtc::THREADS, 1) pa_mass_tc_kernel(MassParams 
                     ok = false;
                     break;
                 }
-            }
-            if ((w.u & 1) != wg) continue;
-            const int tok = w.u * CH + t;
-            const bool in = tok < w.L;
-            const int blk = in ? P.block_table[(size_t)w.b * P.tbl + tok / P.bs] : 0;
-            const bool okb = blk >= 1 && blk < P.num_blocks;
-            float ts = 1.f;
-            if (KV == PA_E4M3 && P.k_mode == PA_SCALE_TOKEN && in && okb)
-                ts = __ldg(reinterpret_cast<const float *>(P.k_pool + (size_t)blk * P.k_block + P.k_codes) +
-                           (size_t)w.g * P.bs + tok % P.bs);
-            float *out = P.mass + ((size_t)w.b * P.Hkv + w.g) * P.max_ctx + tok;
-            const float dec = w.c == 0 ? P.decay : 1.f;
-            const float old = in && dec != 0.f ? *out : 0.f;
-            const float4 *cst = reinterpret_cast<const float4 *>(smem + Y::CST_OFF) + (seg & 1) * (Y::NMAX / 2);
-            const int *vs = reinterpret_cast<const int *>(smem + Y::VIS_OFF) + (seg & 1) * Y::NMAX;
-            bool masked = false;
-            if (w.u * CH + CH > w.L - P.n) {
-                masked = true;
-            } else {  // a row that saw nothing (lse = -inf) is masked everywhere
                 int mn = 0x7FFFFFFF;
                 for (int r = lane; r < rp; r += 32) mn = min(mn, vs[r]);
-                masked = __any_sync(0xffffffffu, mn <= 0);
-            }
-            ok = warp_wait_u(&bars[Y::B_SFULL + wg], sphase & 1, abort, err);
-            if (!ok) break;
-            ++sphase;
-            tc_fence_after();
-            float tot[4] = {0.f, 0.f, 0.f, 0.f};
-            for (int r0 = 0; r0 < rp; r0 += 8) {
-                uint32_t z[8], z2[8];
-                tmem_ld8_nowait(tl + (uint32_t)r0, z);
-                if (nt == 2) tmem_ld8_nowait(tl + (uint32_t)(rp + r0), z2);
-                tmem_ld_wait();
+                const bool seg_off = __any_sync(0xffffffffu, mn <= 0);
+                const ulonglong2 *cst2 = reinterpret_cast<const ulonglong2 *>(cst);
+                // ---- its tiles
+                for (int u = u1; u < w.ue; u += 2) {
+                    const int tok = u * CH + t;
+                    const bool in = tok < w.L, okb = f_blk >= 1 && f_blk < P.num_blocks;
+                    const float old = f_old;
+                    float ts = 1.f;
+                    if (KV == PA_E4M3 && P.k_mode == PA_SCALE_TOKEN && in && okb)
+                        ts = __ldg(reinterpret_cast<const float *>(P.k_pool + (size_t)f_blk * P.k_block + P.k_codes) +
+                                   (size_t)w.g * P.bs + tok % P.bs);
+                    fetch_token(u + 2);
+                    // some row may not see some token of the tile (or saw nothing at all: lse = -inf)
+                    const bool masked = seg_off || u * CH + CH > w.L - P.n;
+                    ok = warp_wait_u(&bars[Y::B_SFULL + wg], sphase & 1, abort, err);
+                    if (!ok) break;
+                    ++sphase;
+                    tc_fence_after();
+                    const uint64_t ts2 = f2(ts, ts);
+                    uint64_t tot[2] = {0, 0};
+                    auto add_rows = [&](auto ncol, auto terms, int r0) {
+                        constexpr int C = decltype(ncol)::value, NT = decltype(terms)::value;
+                        float z[C], z2[NT == 2 ? C : 1];
+                        if constexpr (C == 32) {
+                            tmem_ld32_nowait(tl + (uint32_t)r0, z);
+                            tmem_wait32(z);
+                        } else {
+                            tmem_ld16_nowait(tl + (uint32_t)r0, reinterpret_cast<uint32_t *>(z));
+                            if constexpr (NT == 2)
+                                tmem_ld16_nowait(tl + (uint32_t)(rp + r0), reinterpret_cast<uint32_t *>(z2));
+                            tmem_wait16(z);
+                            if constexpr (NT == 2) tmem_wait16(z2);
+                        }
 #pragma unroll
-                for (int e = 0; e < 8; e += 2) {
-                    const float4 c4 = cst[(r0 + e) >> 1];
-                    float a = __uint_as_float(z[e]), d = __uint_as_float(z[e + 1]);
-                    if (nt == 2) {
-                        a += __uint_as_float(z2[e]);
-                        d += __uint_as_float(z2[e + 1]);
-                    }
-                    const float pa_ = ex2(fmaf(a * ts, c4.x, c4.z) * LOG2E);
-                    const float pd = ex2(fmaf(d * ts, c4.y, c4.w) * LOG2E);
+                        for (int e = 0; e < C; e += 2) {
+                            const ulonglong2 c = cst2[(r0 + e) >> 1];  // {scales, -lse} of two rows
+                            uint64_t d = f2(z[e], z[e + 1]);
+                            if constexpr (NT == 2) d = add2(d, f2(z2[e], z2[e + 1]));
+                            if (KV == PA_E4M3) d = mul2(d, ts2);
+                            d = mul2(fma2(d, c.x, c.y), l2e);
+                            float a, b;
+                            f2_split(d, a, b);
+                            tot[(e >> 1) & 1] = add2(tot[(e >> 1) & 1], f2(ex2(a), ex2(b)));
+                        }
+                    };
+                    float got = 0.f;
                     if (masked) {
-                        const int2 v2 = *reinterpret_cast<const int2 *>(vs + r0 + e);
-                        tot[e & 2] += tok < v2.x ? pa_ : 0.f;
-                        tot[(e & 2) + 1] += tok < v2.y ? pd : 0.f;
+                        got = masked_sum(tl, rp, nt, cst, vs, tok, ts);
                     } else {
-                        tot[e & 2] += pa_;
-                        tot[(e & 2) + 1] += pd;
+                        using I16 = std::integral_constant<int, 16>;
+                        using I1 = std::integral_constant<int, 1>;
+                        int r0 = 0;
+                        if (nt == 2) {
+#pragma unroll 1
+                            for (; r0 < rp; r0 += 16) add_rows(I16(), std::integral_constant<int, 2>(), r0);
+                        } else {
+#pragma unroll 1
+                            for (; r0 + 32 <= rp; r0 += 32) add_rows(std::integral_constant<int, 32>(), I1(), r0);
+                            if (r0 < rp) add_rows(I16(), I1(), r0);
+                        }
+                        float a, b;
+                        f2_split(add2(tot[0], tot[1]), a, b);
+                        got = a + b;
+                    }
+                    tc_fence_before();
+                    warp_arrive(&bars[Y::B_SFREE + wg]);
+                    if (in) {
+                        mass[tok] = !okb ? NaN : dec != 0.f ? fmaf(dec, old, got) : got;
+                        if (!okb) err |= PA_DEV_ERR_BLOCK_ID;
                     }
                 }
             }
-            tc_fence_before();
-            warp_arrive(&bars[Y::B_SFREE + wg]);
-            if (in) {
-                const float got = (tot[0] + tot[1]) + (tot[2] + tot[3]);
-                *out = !okb ? NaN : dec != 0.f ? fmaf(dec, old, got) : got;
-                if (!okb) err |= PA_DEV_ERR_BLOCK_ID;
-            }
+            if (!ok) break;
         }
-        if (!ok) {  // a wait ran out: the rest of the share is NaN
-            for (; !w.end; walk_next(w, P, ps, chunks)) {
-                const int tok = w.u * CH + t;
-                if ((w.u & 1) == wg && tok < w.L) P.mass[((size_t)w.b * P.Hkv + w.g) * P.max_ctx + tok] = NaN;
-            }
+        if (!ok) {  // a wait ran out: the tiles of the whole share are NaN
+            w.x = x0;
+            w.end = false;
+            for (walk_piece(w, P, ps); !w.end; walk_piece(w, P, ps))
+                for (int u = w.ua + ((w.ua ^ wg) & 1); u < w.ue; u += 2)
+                    if (u * CH + t < w.L) P.mass[((size_t)w.b * P.Hkv + w.g) * P.max_ctx + u * CH + t] = NaN;
         }
     } else {
-        // ================================================== MMA issue (lane 0)
-        if (lane == 0) {
-            const int rp = (rows_c + 7) / 8 * 8, n = nt * rp;
+        regs_dec<REGS_MMA>();
+        // ================================================== MMA issue (one thread)
+        if (warp == W_MMA && lane == 0) {
+            const int rp = rows_c, n = nt * rp;
             constexpr uint32_t FMT = BF ? (1u << 7) | (1u << 10) : 0u;
-            const uint32_t id = idesc(CH, (n + 15) / 16 * 16, 0) | FMT;
+            const uint32_t id = idesc(CH, n, 0) | FMT;
             int i = 0, seg = -1, pb = -1, pg = -1, pc = -1, pua = -1;
             int used[2] = {0, 0};
             for (; !w.end; ++i) {
@@ -475,6 +581,11 @@ cudaError_t launch_tc(const MassParams &P, int nt, int sms, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const unsigned long long bit = 1ull << (dev & 63);
     if (dev >= 64 || !(done.load(std::memory_order_relaxed) & bit)) {
+        // the register split draws on what the block was launched with
+        cudaFuncAttributes at;
+        e = cudaFuncGetAttributes(&at, pa_mass_tc_kernel<D, KV>);
+        if (e != cudaSuccess) return e;
+        if (at.numRegs < mtc::REGS_LAUNCH) return cudaErrorLaunchOutOfResources;
         e = cudaFuncSetAttribute(pa_mass_tc_kernel<D, KV>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
         if (e != cudaSuccess) return e;
         done.fetch_or(bit, std::memory_order_relaxed);
