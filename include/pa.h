@@ -584,7 +584,7 @@ PA_API pa_status pa_attention_mass(const pa_problem *p, float decay, const void 
  *                the device error word (pa_get_error).
  * Blocks that hold moved or filled slots must not be shared between requests.
  * Rows of whole 16-byte pieces (head_dim * bits / 8) and max_context_len <=
- * 2^20 are supported; other problems return PA_ERR_UNSUPPORTED.  A request
+ * 2^19 are supported; other problems return PA_ERR_UNSUPPORTED.  A request
  * whose length or history breaks the contract (PA_DEV_ERR_CONTEXT_LEN) or
  * which has a block id outside [1, num_blocks) (PA_DEV_ERR_BLOCK_ID) is left
  * unevicted: nothing of it is written but lens_out (its length) and

@@ -137,23 +137,26 @@ def fp4_logits(w, p, out, workspace, stream=None) -> None:
                     _ptr(w.block_table), _ptr(workspace), workspace.numel(), _ptr(out), stream_handle(stream))
 
 
-def _need(t, name: str, dtype=None, numel: int = 0, contiguous: bool = True) -> int:
-    """The address of a CUDA tensor of at least numel elements on the current device, or a ValueError."""
+def _dtypes():
     import torch
-    if t is None:
-        return None
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name}: a tensor on the current CUDA device is needed, got {t.device}")
-    if dtype is not None and str(t.dtype) != dtype:
-        raise ValueError(f"{name}: {dtype} is needed, got {t.dtype}")
-    if t.numel() < numel:
-        raise ValueError(f"{name}: {numel} elements are needed, got {t.numel()}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name}: a contiguous tensor is needed")
+    return {0: torch.float32, 1: torch.float16, 2: torch.bfloat16}
+
+
+def _need(t, name: str, dtype, numel: int, dev: int) -> int:
+    """The address of a contiguous CUDA tensor of at least numel elements on the current device dev, or a ValueError
+    (dtype None: any)."""
+    if t.get_device() != dev or (dtype is not None and t.dtype is not dtype) or t.numel() < numel \
+            or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous tensor of at least {numel} elements of {dtype or 'any type'} on "
+                         f"device {dev} is needed, got {tuple(t.shape)} {t.dtype} on {t.device}, strides {t.stride()}")
     return t.data_ptr()
 
 
-_TORCH_OF = {0: "torch.float32", 1: "torch.float16", 2: "torch.bfloat16"}
+def _here(stream):
+    """(torch, the current CUDA device, the stream's handle); stream None: the current one."""
+    import torch
+    dev = torch.cuda.current_device()
+    return torch, dev, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def prompt_problem(*, num_seqs: int, total_q: int, total_k: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
@@ -179,24 +182,25 @@ def prompt_attention(p, q, k, v, cu_q, cu_k, out, lse=None, dev_error=None, stre
     [total_q, Hq], dev_error an optional int32 tensor of one element that
     collects the error bits."""
     b = binding()
-    dt, D = _TORCH_OF.get(p.dtype), p.head_dim
+    torch, dev, st = _here(stream)
+    types = _dtypes()
+    dt, D, tq, tk, Hq, Hkv = types.get(p.dtype), p.head_dim, p.total_q, p.total_k, p.num_q_heads, p.num_kv_heads
 
     def rows(t, name, heads, stride, n):
-        if t.dim() != 3 or tuple(t.shape[1:]) != (heads, D) or t.shape[0] < n or (
-                n > 0 and (t.stride(2) != 1 or t.stride(1) != D)):
-            raise ValueError(f"{name}: [{n}, {heads}, {D}] rows are needed, got {tuple(t.shape)} strides {t.stride()}")
-        if n > 1 and t.stride(0) != (stride or heads * D):
-            raise ValueError(f"{name}: rows {stride or heads * D} elements apart are needed, got {t.stride(0)}")
-        return _need(t, name, dt, contiguous=False)
+        stride = stride or heads * D
+        if t.get_device() != dev or t.dtype is not dt or t.dim() != 3 or t.shape[0] < n or t.shape[1:] != (heads, D) \
+                or (n > 0 and t.stride() != (stride, D, 1) and not (n == 1 and t.stride()[1:] == (D, 1))):
+            raise ValueError(f"{name}: [{n}, {heads}, {D}] rows of {dt}, {stride} elements apart, on device {dev} are "
+                             f"needed, got {tuple(t.shape)} {t.dtype} on {t.device}, strides {t.stride()}")
+        return t.data_ptr()
 
-    b.pa_prompt_attention(p, rows(q, "q", p.num_q_heads, p.q_stride, p.total_q),
-                          rows(k, "k", p.num_kv_heads, p.k_stride, p.total_k),
-                          rows(v, "v", p.num_kv_heads, p.v_stride, p.total_k),
-                          _need(cu_q, "cu_q", "torch.int32", p.num_seqs + 1),
-                          _need(cu_k, "cu_k", "torch.int32", p.num_seqs + 1),
-                          _need(out, "out", _TORCH_OF.get(p.out_dtype), p.total_q * p.num_q_heads * D),
-                          _need(lse, "lse", "torch.float32", p.total_q * p.num_q_heads),
-                          _need(dev_error, "dev_error", "torch.int32", 1), stream_handle(stream))
+    i32 = torch.int32
+    b.pa_prompt_attention(p, rows(q, "q", Hq, p.q_stride, tq), rows(k, "k", Hkv, p.k_stride, tk),
+                          rows(v, "v", Hkv, p.v_stride, tk), _need(cu_q, "cu_q", i32, p.num_seqs + 1, dev),
+                          _need(cu_k, "cu_k", i32, p.num_seqs + 1, dev),
+                          _need(out, "out", types.get(p.out_dtype), tq * Hq * D, dev),
+                          None if lse is None else _need(lse, "lse", torch.float32, tq * Hq, dev),
+                          None if dev_error is None else _need(dev_error, "dev_error", i32, 1, dev), st)
 
 
 def attention_mass(w, p, lse, mass, decay: float = 1.0, dev_error=None, stream=None) -> None:
@@ -205,15 +209,17 @@ def attention_mass(w, p, lse, mass, decay: float = 1.0, dev_error=None, stream=N
     receives from the query rows w.q, given their log-sum-exps lse
     (float32 [B, n, Hq], as pa_attention wrote them)."""
     b = binding()
-    B, n = p.batch, p.next_n
-    b.pa_attention_mass(p, decay, _need(w.q, "q", _TORCH_OF.get(p.q_dtype), B * n * p.num_q_heads * p.head_dim_k),
-                        _need(w.k_pool, "k_pool"),
-                        _need(w.block_table, "block_table", "torch.int32", B * p.max_blocks_per_seq),
-                        _need(w.context_lens, "context_lens", "torch.int32", B),
-                        _need(w.k_scale, "k_scale", "torch.float32"),
-                        _need(lse, "lse", "torch.float32", B * n * p.num_q_heads),
-                        _need(mass, "mass", "torch.float32", B * p.num_kv_heads * p.max_context_len),
-                        _need(dev_error, "dev_error", "torch.int32", 1), stream_handle(stream))
+    torch, dev, st = _here(stream)
+    B, rows = p.batch, p.batch * p.next_n * p.num_q_heads
+    i32, f32 = torch.int32, torch.float32
+    b.pa_attention_mass(p, decay, _need(w.q, "q", _dtypes().get(p.q_dtype), rows * p.head_dim_k, dev),
+                        _need(w.k_pool, "k_pool", None, 1, dev),
+                        _need(w.block_table, "block_table", i32, B * p.max_blocks_per_seq, dev),
+                        _need(w.context_lens, "context_lens", i32, B, dev),
+                        None if w.k_scale is None else _need(w.k_scale, "k_scale", f32, 1, dev),
+                        _need(lse, "lse", f32, rows, dev),
+                        _need(mass, "mass", f32, B * p.num_kv_heads * p.max_context_len, dev),
+                        None if dev_error is None else _need(dev_error, "dev_error", i32, 1, dev), st)
 
 
 def evict_workspace_bytes(p, budget: int) -> int:
@@ -229,12 +235,14 @@ def evict(w, p, budget: int, mass, positions, history, mass_out, positions_out, 
     [B, 2]; the *_out tensors may be the inputs themselves and lens_out
     w.context_lens."""
     b = binding()
+    torch, dev, st = _here(stream)
     B, rows = p.batch, p.batch * p.num_kv_heads * p.max_context_len
-    i32, f32 = "torch.int32", "torch.float32"
-    b.pa_evict(p, budget, sinks, recent, _need(mass, "mass", f32, rows), _need(positions, "positions", i32, rows),
-               _need(history, "history", i32, 2 * B),
-               _need(w.block_table, "block_table", i32, B * p.max_blocks_per_seq),
-               _need(w.context_lens, "context_lens", i32, B), _need(w.k_pool, "k_pool"), _need(w.v_pool, "v_pool"),
-               _need(mass_out, "mass_out", f32, rows), _need(positions_out, "positions_out", i32, rows),
-               _need(history_out, "history_out", i32, 2 * B), _need(lens_out, "lens_out", i32, B),
-               _need(workspace, "workspace", "torch.uint8"), workspace.numel(), stream_handle(stream))
+    i32, f32 = torch.int32, torch.float32
+    b.pa_evict(p, budget, sinks, recent, _need(mass, "mass", f32, rows, dev),
+               _need(positions, "positions", i32, rows, dev), _need(history, "history", i32, 2 * B, dev),
+               _need(w.block_table, "block_table", i32, B * p.max_blocks_per_seq, dev),
+               _need(w.context_lens, "context_lens", i32, B, dev), _need(w.k_pool, "k_pool", None, 1, dev),
+               None if w.v_pool is None else _need(w.v_pool, "v_pool", None, 1, dev),
+               _need(mass_out, "mass_out", f32, rows, dev), _need(positions_out, "positions_out", i32, rows, dev),
+               _need(history_out, "history_out", i32, 2 * B, dev), _need(lens_out, "lens_out", i32, B, dev),
+               _need(workspace, "workspace", torch.uint8, 1, dev), workspace.numel(), st)

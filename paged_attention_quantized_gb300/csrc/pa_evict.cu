@@ -2,13 +2,15 @@
 //
 // Selection (pa_evict_select_kernel), one CTA per (request, kv head): every
 // slot gets a 32-bit key that orders as its mass does (protected slots the
-// largest key, NaN the smallest), the left-th largest key is found bit by bit
-// by counting keys at or above a candidate, and the slots above it plus the
-// first of those equal to it are kept.  Keys stay in registers (up to 32
-// slots per lane; longer rows read the mass again from L2 for every count).
-// Ordered ranks of the free slots below `left` and of the kept ones at or past
-// it come from warp ballots and one scan over the warps; their i-th entries
-// pair up as the moves of the row.
+// largest key, NaN the smallest), the left-th largest key is found digit by
+// digit (11, 11, 10 bits) from histograms in shared memory until at most 32
+// keys are left in question, which one warp then ranks; the slots above it plus
+// the first of those equal to it are kept.  Keys stay in registers (up to 32
+// slots per thread; longer rows read the mass again from L2 for every pass).
+// The kept slots become a bitmap in shared memory, one ballot per 32 slots, and
+// the number kept before each word comes from one scan: the rank of a free slot
+// s below `left` is s less the kept ones before it, that of a kept slot at or
+// past `left` is the kept ones between; the i-th of both pair up as the moves.
 //
 // Moves (pa_evict_move_kernel): one thread per 16-byte piece of a moved K or V
 // row.  Sources lie at or past `left`, destinations below it, so no row is
@@ -45,8 +47,7 @@ struct EvictParams {
 
 namespace evict {
 
-constexpr int THREADS = 1024, NW = THREADS / 32;
-constexpr int MOVE_THREADS = 256, MOVE_ROWS = 32;  // rows of one CTA of the move kernel
+constexpr int MOVE_THREADS = 256, MOVE_ROWS = 128;  // rows of one CTA of the move kernel
 
 // order-preserving key of a mass: larger mass, larger key; NaN below all (0)
 __device__ __forceinline__ uint32_t mass_key(float v) {
@@ -55,17 +56,47 @@ __device__ __forceinline__ uint32_t mass_key(float v) {
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// KPT: slots per lane kept in registers (KPT * 1024 slots), 0 = read again each time
-template <int KPT>
-__global__ void __launch_bounds__(THREADS) pa_evict_select_kernel(EvictParams P) {
+// Exclusive prefix sum of v over the block's threads, and the total
+template <int NW>
+__device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t *s_warp, uint64_t &total) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint64_t x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) s_warp[warp] = x;
+    __syncthreads();
+    uint64_t before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+        const uint64_t t = s_warp[w];
+        if (w < warp) before += t;
+        all += t;
+    }
+    __syncthreads();
+    total = all;
+    return before + x - v;
+}
+
+// KPT: slots per thread kept in registers (slot i * THREADS + thread), 0 = read again each time
+template <int THREADS, int KPT>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) pa_evict_select_kernel(EvictParams P) {
+    constexpr int NW = THREADS / 32;
     grid_dependents_launch();  // the move kernel may queue up behind
-    __shared__ int s_cnt[32];
-    __shared__ int s_warp[3][NW];
-    __shared__ uint32_t s_err;
+    constexpr int BINS = 2048, BPT = BINS / THREADS;
+    extern __shared__ uint32_t s_map[];  // one bit per slot, 32 consecutive slots a word; then the kept ones before each word
+    __shared__ int s_hist[BINS], s_n, s_bin, s_over, s_in;
+    __shared__ uint64_t s_warp[NW];
+    __shared__ uint32_t s_few[32], s_pick, s_err;
+    __shared__ int s_cut;
     const int g = blockIdx.x, b = blockIdx.y;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (tid < 32) s_cnt[tid] = 0;
-    if (tid == 0) s_err = 0;
+    if (tid == 0) {
+        s_n = 0;
+        s_err = 0;
+    }
     __syncthreads();
     const int L = P.context_lens[b];
     const int base = P.history[2 * b], dropped = P.history[2 * b + 1];
@@ -81,16 +112,9 @@ __global__ void __launch_bounds__(THREADS) pa_evict_select_kernel(EvictParams P)
             badid |= blk < 1 || blk >= P.num_blocks;
         }
         if (badid) s_err = PA_DEV_ERR_BLOCK_ID;
-        __syncthreads();
-        err = s_err;
     }
     const int left = min(L, P.budget);
-    if (g == 0 && tid == 0) P.req[b] = err ? make_int4(L, base, dropped, (int)err) : make_int4(left, left, dropped + L - left, 0);
     const size_t rowi = (size_t)b * P.Hkv + g;
-    if (err) {
-        if (tid == 0) P.counts[rowi] = 0;
-        return;
-    }
     const float *mass = P.mass + rowi * P.max_ctx;
     const int32_t *pos_in = P.positions + rowi * P.max_ctx;
     float *mass_out = P.mass_out + rowi * P.max_ctx;
@@ -101,116 +125,189 @@ __global__ void __launch_bounds__(THREADS) pa_evict_select_kernel(EvictParams P)
         const int p = pos_of(s);
         return (p < P.sinks || p >= newest) ? 0xFFFFFFFFu : mass_key(mass[s]);
     };
-    // warp w holds slots [w * per, (w + 1) * per), 32 consecutive ones at a time
-    const int strips = (L + THREADS - 1) / THREADS;  // strips of 32 per warp
-    const int per = strips * 32, s0 = warp * per + lane;
+    const int strips = err ? 0 : (L + THREADS - 1) / THREADS;  // slots of this thread: i * THREADS + tid, i < strips
     constexpr int KR = KPT > 0 ? KPT : 1;
     uint32_t key[KR];
-    if (KPT > 0) {
+    if constexpr (KPT > 0) {
+        // loads first, eight of them in flight before the first is used
 #pragma unroll
-        for (int i = 0; i < KR; ++i) {
-            const int s = s0 + 32 * i;
-            key[i] = (i < strips && s < L) ? key_of(s) : 0u;
-        }
-    }
-    // ---- the left-th largest key T: the largest T with at least `left` keys >= T
-    uint32_t T = 0;
-    int above = L;  // keys >= T
-    if (left < L) {
-        for (int bit = 31; bit >= 0; --bit) {
-            const uint32_t cand = T | (1u << bit);
-            int n = 0;
-            if (KPT > 0) {
+        for (int i0 = 0; i0 < KR; i0 += 8) {
+            float v[8];
+            int p[8];
 #pragma unroll
-                for (int i = 0; i < KR; ++i) n += key[i] >= cand ? 1 : 0;  // (unused slots have key 0 < cand)
-            } else {
-                for (int i = 0; i < strips; ++i) {
-                    const int s = s0 + 32 * i;
-                    n += (s < L && key_of(s) >= cand) ? 1 : 0;
-                }
+            for (int i = 0; i < 8; ++i) {
+                const int s = (i0 + i) * THREADS + tid;
+                v[i] = !err && s < L ? mass[s] : 0.f;
             }
-            n = __reduce_add_sync(0xffffffffu, n);
-            if (lane == 0 && n) atomicAdd(&s_cnt[bit], n);
-            __syncthreads();
-            n = s_cnt[bit];
-            if (n >= left) {
-                T = cand;
-                above = n;
-                if (n == left) break;  // exactly these
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int s = (i0 + i) * THREADS + tid;
+                p[i] = !err && s < base ? pos_in[s] : dropped + s;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const bool always = p[i] < P.sinks || p[i] >= newest;
+                key[i0 + i] = err || (i0 + i) * THREADS + tid >= L ? 0u : always ? 0xFFFFFFFFu : mass_key(v[i]);
             }
         }
     }
-    // `above` keys are >= T; of those equal to T the last `above - left` go
-    // ---- ranks: ties (key == T), then free slots below left and kept ones past it
-    auto each_strip = [&](auto &&body) {  // body(slot, in the request, key)
+    __syncthreads();
+    if (err == 0) err = s_err;
+    if (g == 0 && tid == 0)
+        P.req[b] = err ? make_int4(L, base, dropped, (int)err) : make_int4(left, left, dropped + L - left, 0);
+    if (err) {
+        if (tid == 0) P.counts[rowi] = 0;
+        return;
+    }
+    auto each = [&](auto &&body) {  // body(slot, in the request, key): whole warps, 32 consecutive slots each
         if constexpr (KPT > 0) {
 #pragma unroll
             for (int i = 0; i < KR; ++i)
-                if (i < strips) body(s0 + 32 * i, s0 + 32 * i < L, key[i]);
+                if (i < strips) body(i * THREADS + tid, i * THREADS + tid < L, key[i]);
         } else {
             for (int i = 0; i < strips; ++i) {
-                const int s = s0 + 32 * i;
+                const int s = i * THREADS + tid;
                 body(s, s < L, s < L ? key_of(s) : 0u);
             }
         }
     };
-    int ties = 0;
-    each_strip([&](int, bool in, uint32_t kk) { ties += __popc(__ballot_sync(0xffffffffu, in && kk == T)); });
-    if (lane == 0) s_warp[0][warp] = ties;
-    __syncthreads();
-    int all_ties = 0, ties_before = 0;
-    for (int w = 0; w < NW; ++w) {
-        const int t = s_warp[0][w];
-        if (w < warp) ties_before += t;
-        all_ties += t;
-    }
-    const int keep_ties = all_ties - (above - left);
-    auto classify = [&](auto &&visit) {
-        int tb = ties_before;
-        each_strip([&](int s, bool in, uint32_t kk) {
-            const unsigned tm = __ballot_sync(0xffffffffu, in && kk == T);
-            const bool kept = in && (kk > T || (kk == T && tb + __popc(tm & ((1u << lane) - 1)) < keep_ties));
-            tb += __popc(tm);
-            const unsigned fm = __ballot_sync(0xffffffffu, in && !kept && s < left);
-            const unsigned mm = __ballot_sync(0xffffffffu, kept && s >= left);
-            visit(s, kept, in, fm, mm);
-        });
-    };
-    int nfree = 0, nmove = 0;
-    classify([&](int, bool, bool, unsigned fm, unsigned mm) {
-        nfree += __popc(fm);
-        nmove += __popc(mm);
-    });
-    if (lane == 0) {
-        s_warp[1][warp] = nfree;
-        s_warp[2][warp] = nmove;
-    }
-    __syncthreads();
-    int f0 = 0, m0 = 0, moves = 0;
-    for (int w = 0; w < NW; ++w) {
-        if (w < warp) {
-            f0 += s_warp[1][w];
-            m0 += s_warp[2][w];
-        }
-        moves += s_warp[2][w];
-    }
-    int32_t *dst = P.lists + rowi * 2 * P.cap, *src = dst + P.cap;
-    classify([&](int s, bool kept, bool in, unsigned fm, unsigned mm) {
-        const unsigned lt = (1u << lane) - 1;
-        if (in && s < left) {
-            if (kept) {  // stays (its own entry: no other thread reads it)
-                const int p = pos_of(s);
-                mass_out[s] = mass[s];
-                pos_out[s] = p;
-            } else {
-                dst[f0 + __popc(fm & lt)] = s;
+    // ---- the left-th largest key T: the largest T with at least `left` keys >= T
+    uint32_t T = 0;
+    int above = L, over = 0;  // keys >= T, keys past the interval in question
+    for (int shift = 21; left < L; shift = max(0, shift - 11)) {
+        // histogram of the keys of [T, T + 2^min(32, shift + 11)) by their next digit
+        for (int i = tid; i < BINS; i += THREADS) s_hist[i] = 0;
+        __syncthreads();
+        each([&](int, bool in, uint32_t k) {
+            const uint32_t d = (k - T) >> shift;
+            const bool mine = in && k >= T && d < BINS;
+            const unsigned m = __ballot_sync(0xffffffffu, mine);
+            if (m == 0) return;
+            const uint32_t d0 = __shfl_sync(0xffffffffu, d, __ffs(m) - 1);
+            if (__all_sync(0xffffffffu, !mine || d == d0)) {  // (long runs of equal masses: one addition)
+                if (lane == 0) atomicAdd(&s_hist[d0], __popc(m));
+            } else if (mine) {
+                atomicAdd(&s_hist[d], 1);
             }
-        } else if (kept) {
-            src[m0 + __popc(mm & lt)] = s;
+        });
+        __syncthreads();
+        // the digit where the count from the top reaches `left`
+        int c = 0;
+#pragma unroll
+        for (int i = 0; i < BPT; ++i) c += s_hist[BINS - 1 - (tid * BPT + i)];
+        uint64_t total;
+        int before = over + (int)block_scan<NW>((uint64_t)c, s_warp, total);
+        if (before < left && left <= before + c) {
+            for (int i = 0; i < BPT; ++i) {
+                const int bin = BINS - 1 - (tid * BPT + i), h = s_hist[bin];
+                if (left <= before + h) {
+                    s_bin = bin;
+                    s_over = before;
+                    s_in = h;
+                    break;
+                }
+                before += h;
+            }
         }
-        f0 += __popc(fm);
-        m0 += __popc(mm);
+        __syncthreads();
+        T += (uint32_t)s_bin << shift;
+        over = s_over;
+        above = over + s_in;
+        if (above == left || shift == 0) break;
+        if (above - over <= 32) {
+            // few keys are left in [T, T + 2^shift): list them, and rank them in one warp
+            const uint32_t span = 1u << shift;
+            each([&](int, bool in, uint32_t k) {
+                if (in && k - T < span) s_few[atomicAdd(&s_n, 1)] = k;
+            });
+            __syncthreads();
+            if (warp == 0) {
+                const int m = above - over;
+                const uint32_t k = lane < m ? s_few[lane] : 0u;
+                int more = 0;  // keys at or above this lane's
+                for (int i = 0; i < m; ++i) more += __shfl_sync(0xffffffffu, k, i) >= k ? 1 : 0;
+                // the largest key with at least left - over of the few at or above it
+                const bool ok = lane < m && over + more >= left;
+                const uint32_t pick = __reduce_max_sync(0xffffffffu, ok ? k : T);
+                if (ok && k == pick) {  // (equal keys agree)
+                    s_pick = pick;
+                    s_n = over + more;
+                }
+            }
+            __syncthreads();
+            T = s_pick;
+            above = s_n;
+            break;
+        }
+    }
+    // ---- `above` keys are >= T; of those equal to T the last above - left in slot order go:
+    // the ones from slot s_cut on
+    const int words = (L + 31) / 32, wpt = (words + THREADS - 1) / THREADS;
+    const int w0 = min(words, tid * wpt), w1 = min(words, w0 + wpt);  // this thread's words in the scans
+    if (tid == 0) s_cut = L;
+    if (above > left) {
+        each([&](int s, bool in, uint32_t k) {
+            const unsigned m = __ballot_sync(0xffffffffu, in && k == T);
+            if (lane == 0 && in) s_map[s >> 5] = m;
+        });
+        __syncthreads();
+        int n = 0;
+        for (int w = w0; w < w1; ++w) n += __popc(s_map[w]);
+        uint64_t total;
+        int before = (int)block_scan<NW>((uint64_t)n, s_warp, total);
+        const int keep = (int)total - (above - left);  // ties that stay
+        if (before < keep + 1 && keep < before + n) {   // the first one to go is among this thread's words
+            for (int w = w0; w < w1; ++w) {
+                unsigned m = s_map[w];
+                const int c = __popc(m);
+                if (keep < before + c) {
+                    for (int i = before; i < keep; ++i) m &= m - 1;
+                    s_cut = w * 32 + __ffs(m) - 1;
+                    break;
+                }
+                before += c;
+            }
+        }
+        __syncthreads();
+    }
+    __syncthreads();
+    const int cut = s_cut;
+    each([&](int s, bool in, uint32_t k) {
+        const unsigned m = __ballot_sync(0xffffffffu, in && (k > T || (k == T && s < cut)));
+        if (lane == 0 && in) s_map[s >> 5] = m;
     });
+    __syncthreads();
+    // ---- how many are kept before each word, and below left
+    uint32_t *s_before = s_map + words;
+    int n = 0;
+    for (int w = w0; w < w1; ++w) n += __popc(s_map[w]);
+    uint64_t total;
+    int at = (int)block_scan<NW>((uint64_t)n, s_warp, total);
+    for (int w = w0; w < w1; ++w) {
+        s_before[w] = at;
+        at += __popc(s_map[w]);
+    }
+    __syncthreads();
+    auto kept_before = [&](int s) -> int {  // of slots below s, s < 32 * words
+        return (int)s_before[s >> 5] + __popc(s_map[s >> 5] & ((1u << (s & 31)) - 1));
+    };
+    const int stay = left < L ? kept_before(left) : left, moves = left - stay;
+    int32_t *dst = P.lists + rowi * 2 * P.cap, *src = dst + P.cap;
+    // ---- the kept slots below left keep their entries (their own: no other
+    // thread reads them), the free ones and the kept ones past left are listed
+#pragma unroll 4
+    for (int s = tid; s < left; s += THREADS) {
+        if ((s_map[s >> 5] >> (s & 31)) & 1u) {
+            const int p = pos_of(s);
+            mass_out[s] = mass[s];
+            pos_out[s] = p;
+        } else {
+            dst[s - kept_before(s)] = s;
+        }
+    }
+#pragma unroll 4
+    for (int s = left + tid; s < L; s += THREADS)
+        if ((s_map[s >> 5] >> (s & 31)) & 1u) src[kept_before(s) - stay] = s;
     __syncthreads();
     for (int i = tid; i < moves; i += THREADS) {
         const int s = src[i], d = dst[i];
@@ -268,26 +365,33 @@ __global__ void __launch_bounds__(MOVE_THREADS) pa_evict_move_kernel(EvictParams
                 *reinterpret_cast<const float *>(P.v_pool + (long long)bs_ * P.v_block + P.v_codes + rs * 4);
     }
     __syncthreads();
-    const int kp = P.k_row / 16, pieces = kp + P.v_row / 16, total = rows * pieces;
+    const int kp = P.k_row / 16, pieces = kp + P.v_row / 16;
+    const int dr = MOVE_THREADS / pieces, dp = MOVE_THREADS - dr * pieces;
+    int r = tid / pieces, p = tid - r * pieces;
     constexpr int UN = 4;
-    for (int base = tid; base < total; base += MOVE_THREADS * UN) {
+    while (r < rows) {
         uint4 v[UN];
         uint4 *to[UN];
 #pragma unroll
         for (int q = 0; q < UN; ++q) {
-            const int i = base + q * MOVE_THREADS;
-            if (i < total) {
-                const int r = i / pieces, p = i - r * pieces;
+            to[q] = nullptr;
+            if (r < rows) {
                 const bool isk = p < kp;
                 uint8_t *pool = isk ? P.k_pool : P.v_pool;
                 const int o = 16 * (isk ? p : p - kp);
                 v[q] = *reinterpret_cast<const uint4 *>(pool + s_at[r][isk ? 0 : 2] + o);
                 to[q] = reinterpret_cast<uint4 *>(pool + s_at[r][isk ? 1 : 3] + o);
             }
+            r += dr;
+            p += dp;
+            if (p >= pieces) {
+                p -= pieces;
+                ++r;
+            }
         }
 #pragma unroll
         for (int q = 0; q < UN; ++q)
-            if (base + q * MOVE_THREADS < total) *to[q] = v[q];
+            if (to[q]) *to[q] = v[q];
     }
 }
 
@@ -295,6 +399,8 @@ __global__ void __launch_bounds__(MOVE_THREADS) pa_evict_move_kernel(EvictParams
 }  // namespace pa
 
 namespace {
+
+constexpr int MAX_CONTEXT = 1 << 19;  // the select kernel's bitmap and counts: 128 KB of shared memory
 
 struct EvictLayout {
     size_t req, counts, lists, total;
@@ -306,7 +412,7 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 pa_status evict_layout(const pa_problem *p, int32_t budget, EvictLayout *lo) {
     if (p == nullptr || lo == nullptr || p->batch < 0 || p->num_kv_heads < 1 || p->max_context_len < 0 || budget < 1)
         return PA_ERR_INVALID_ARG;
-    if (p->max_context_len > (1 << 20) || (long long)p->batch * p->num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
+    if (p->max_context_len > MAX_CONTEXT || (long long)p->batch * p->num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
     // at most `budget` rows move, and at most the rows past it
     lo->cap = std::max(0, std::min(budget, p->max_context_len - budget));
     const size_t rows = (size_t)p->batch * p->num_kv_heads;
@@ -409,10 +515,18 @@ extern "C" PA_API pa_status pa_evict(const pa_problem *p, int32_t budget, int32_
     P.recent = recent;
     P.cap = lo.cap;
     const dim3 grid((unsigned)p->num_kv_heads, (unsigned)p->batch);
-    const int ctx = p->max_context_len, t = pa::evict::THREADS;
-    if (ctx <= 8 * t) pa::evict::pa_evict_select_kernel<8><<<grid, t, 0, s>>>(P);
-    else if (ctx <= 32 * t) pa::evict::pa_evict_select_kernel<32><<<grid, t, 0, s>>>(P);
-    else pa::evict::pa_evict_select_kernel<0><<<grid, t, 0, s>>>(P);
+    const int ctx = p->max_context_len;
+    const size_t map = ((size_t)ctx + 31) / 32 * 8 + 16;  // the bitmap of kept slots, the counts before its words
+    if (ctx <= 4096) pa::evict::pa_evict_select_kernel<256, 16><<<grid, 256, map, s>>>(P);
+    else if (ctx <= 16384) pa::evict::pa_evict_select_kernel<1024, 16><<<grid, 1024, map, s>>>(P);
+    else if (ctx <= 32768) pa::evict::pa_evict_select_kernel<1024, 32><<<grid, 1024, map, s>>>(P);
+    else {
+        if (map > 36 * 1024 &&
+            cudaFuncSetAttribute(pa::evict::pa_evict_select_kernel<1024, 0>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (1 << 17) + 16) != cudaSuccess)
+            return PA_ERR_CUDA;
+        pa::evict::pa_evict_select_kernel<1024, 0><<<grid, 1024, map, s>>>(P);
+    }
     if (cudaPeekAtLastError() != cudaSuccess) return PA_ERR_CUDA;
     const unsigned chunks = (unsigned)std::max(1, (lo.cap + pa::evict::MOVE_ROWS - 1) / pa::evict::MOVE_ROWS);
     const cudaError_t e = pa::launch_pdl(pa::evict::pa_evict_move_kernel, dim3(chunks, (unsigned)(p->batch * p->num_kv_heads)),

@@ -17,6 +17,7 @@
 // shared evenly by persistent warps; each knows its share from a prefix sum
 // over context_lens that every CTA computes for itself.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "pa_mass.cuh"
@@ -217,17 +218,28 @@ __global__ void __launch_bounds__(THREADS) pa_mass_kernel(MassParams P) {
 template <int D, int KV, int NT>
 cudaError_t launch(const MassParams &P, int sms, cudaStream_t s) {
     const size_t smem = ((size_t)P.B + 1) * 4;
-    auto go = [&](auto kernel) -> cudaError_t {
-        int per = 0;
-        cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, THREADS, smem);
+    auto go = [&](auto kernel, std::atomic<int> *kept) -> cudaError_t {
+        // resident CTAs, asked for once per kernel and device at the largest
+        // prefix-sum array that all of them still fit (more requests: asked again)
+        int dev = 0, per = 0;
+        cudaError_t e = cudaGetDevice(&dev);
         if (e != cudaSuccess) return e;
+        const bool keep = dev < 64 && smem <= 4096;
+        if (keep) per = kept[dev].load(std::memory_order_relaxed);
+        if (per == 0) {
+            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, THREADS, keep ? 4096 : smem);
+            if (e != cudaSuccess) return e;
+            per = std::max(1, per);
+            if (keep) kept[dev].store(per, std::memory_order_relaxed);
+        }
         // no warp without a unit of the longest possible batch
         const long long units = (long long)P.B * P.Hkv * ((P.max_ctx + UT - 1) / UT);
-        const long long ctas = std::min<long long>((long long)sms * std::max(1, per), (units + THREADS / 32 - 1) / (THREADS / 32));
+        const long long ctas = std::min<long long>((long long)sms * per, (units + THREADS / 32 - 1) / (THREADS / 32));
         kernel<<<(unsigned)ctas, THREADS, smem, s>>>(P);
         return cudaPeekAtLastError();
     };
-    return P.R <= 8 ? go(pa_mass_kernel<D, KV, 1, NT>) : go(pa_mass_kernel<D, KV, 2, NT>);
+    static std::atomic<int> kept[2][64];
+    return P.R <= 8 ? go(pa_mass_kernel<D, KV, 1, NT>, kept[0]) : go(pa_mass_kernel<D, KV, 2, NT>, kept[1]);
 }
 
 // query terms: a folded per-channel scale, and f16 queries (11 bits) against

@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(mtc::THREADS, 1) pa_mass_tc_kernel(MassParams 
             while (i < mine) {
                 if (ai < mine && ai - i < 2 * PF) {
                     const int slot = ai % NA;
-                    if (ai >= NA && !warp_wait(&bars[Y::B_AFREE + slot], (ai / NA - 1) & 1, abort, err)) break;
+                    if (ai >= NA && !sleep_wait(&bars[Y::B_AFREE + slot], (ai / NA - 1) & 1, abort, err)) break;
                     const uint32_t dst = sb + Y::A_OFF + slot * Y::A_BYTES;
                     const int left = pl[0].left;
                     runs_of(pl[0]);
@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(mtc::THREADS, 1) pa_mass_tc_kernel(MassParams 
             fetch();
             for (; i < mine; i += 2) {
                 const int slot = i % NA;
-                if (i >= NA && !warp_wait(&bars[Y::B_AFREE + slot], (i / NA - 1) & 1, abort, err)) break;
+                if (i >= NA && !sleep_wait(&bars[Y::B_AFREE + slot], (i / NA - 1) & 1, abort, err)) break;
                 uint8_t *dst = smem + Y::A_OFF + slot * Y::A_BYTES;
                 constexpr int OC = 16 / BITS;  // 16-byte operand chunks per raw piece
 #pragma unroll
@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(mtc::THREADS, 1) pa_mass_tc_kernel(MassParams 
                 fetch_token(u1);
                 // ---- a new segment: its query rows
                 ++seg;
-                if (seg > 0 && !warp_wait(&bars[Y::B_QFREE], (seg - 1) & 1, abort, err)) {
+                if (seg > 0 && !sleep_wait(&bars[Y::B_QFREE], (seg - 1) & 1, abort, err)) {
                     ok = false;
                     break;
                 }
@@ -436,7 +436,7 @@ __global__ void __launch_bounds__(mtc::THREADS, 1) pa_mass_tc_kernel(MassParams 
                 }
                 fence_proxy_async_smem();
                 warp_arrive(&bars[Y::B_QFULL]);
-                if (!warp_wait(&bars[Y::B_QFULL], seg & 1, abort, err)) {
+                if (!sleep_wait(&bars[Y::B_QFULL], seg & 1, abort, err)) {
                     ok = false;
                     break;
                 }
@@ -456,7 +456,7 @@ __global__ void __launch_bounds__(mtc::THREADS, 1) pa_mass_tc_kernel(MassParams 
                     fetch_token(u + 2);
                     // some row may not see some token of the tile (or saw nothing at all: lse = -inf)
                     const bool masked = seg_off || u * CH + CH > w.L - P.n;
-                    ok = warp_wait_u(&bars[Y::B_SFULL + wg], sphase & 1, abort, err);
+                    ok = sleep_wait(&bars[Y::B_SFULL + wg], sphase & 1, abort, err);
                     if (!ok) break;
                     ++sphase;
                     tc_fence_after();
@@ -528,6 +528,7 @@ __global__ void __launch_bounds__(mtc::THREADS, 1) pa_mass_tc_kernel(MassParams 
         // ================================================== MMA issue (one thread)
         if (warp == W_MMA && lane == 0) {
             const int rp = rows_c, n = nt * rp;
+            const uint64_t qpanel = (uint64_t)(n * 128 >> 4);  // descriptor step between channel panels of the rows
             constexpr uint32_t FMT = BF ? (1u << 7) | (1u << 10) : 0u;
             const uint32_t id = idesc(CH, n, 0) | FMT;
             int i = 0, seg = -1, pb = -1, pg = -1, pc = -1, pua = -1;
@@ -539,18 +540,21 @@ __global__ void __launch_bounds__(mtc::THREADS, 1) pa_mass_tc_kernel(MassParams 
                     pg = w.g;
                     pc = w.c;
                     pua = w.ua;
-                    if (!lane_wait(&bars[Y::B_QFULL], seg & 1, abort, err)) break;
+                    if (!sleep_wait<false>(&bars[Y::B_QFULL], seg & 1, abort, err)) break;
                 }
                 const int slot = i % NA, buf = w.u & 1;
-                if (!lane_wait(&bars[Y::B_AFULL + slot], (i / NA) & 1, abort, err)) break;
-                if (used[buf] > 0 && !lane_wait(&bars[Y::B_SFREE + buf], (used[buf] - 1) & 1, abort, err)) break;
+                if (!sleep_wait<false>(&bars[Y::B_AFULL + slot], (i / NA) & 1, abort, err)) break;
+                if (used[buf] > 0 && !sleep_wait<false>(&bars[Y::B_SFREE + buf], (used[buf] - 1) & 1, abort, err)) break;
                 ++used[buf];
                 tc_fence_after();
                 const uint64_t a = sdesc(sb + Y::A_OFF + slot * Y::A_BYTES, 16, 1024, 2);
-                const uint64_t q = sdesc(sb + Y::Q_OFF, 16, 1024, 2);
-                for (int k = 0; k < D / 16; ++k)
-                    mma_f16(tmem + 256u * buf, a + (uint32_t)(((k >> 2) * CH * 128 + 32 * (k & 3)) >> 4),
-                            q + (uint32_t)(((k >> 2) * n * 128 + 32 * (k & 3)) >> 4), id, k > 0 ? 1u : 0u);
+                uint64_t q = sdesc(sb + Y::Q_OFF, 16, 1024, 2);
+#pragma unroll
+                for (int pn = 0; pn < D / 64; ++pn, q += qpanel)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_f16(tmem + 256u * buf, a + (uint32_t)((pn * CH * 128 + 32 * k) >> 4), q + 2u * k, id,
+                                (pn > 0 || k > 0) ? 1u : 0u);
                 mma_commit(&bars[Y::B_SFULL + buf]);
                 mma_commit(&bars[Y::B_AFREE + slot]);
                 walk_next(w, P, ps, chunks);

@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             int u = 0;
             for (; u < units; ++u) {
                 const int slot = u % NS;
-                if (u >= NS && !lane_wait(&bars[Y::B_FREE + slot], ((u / NS) - 1) & 1, abort, err)) break;
+                if (u >= NS && !sleep_wait<false>(&bars[Y::B_FREE + slot], ((u / NS) - 1) & 1, abort, err)) break;
                 const int t = u / NU, half = u % NU;  // tile in the order the products need them
                 bool isv;
                 int j;
@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         constexpr uint32_t FMT = BF16 ? (1u << 7) | (1u << 10) : 0u;
         constexpr uint32_t ID_S = idesc(128, BN, 0) | FMT;
         constexpr uint32_t ID_O = idesc(128, D, 0) | FMT | (1u << 16);  // B = V read MN-major
-        auto full = [&](int u) { return lane_wait(&bars[Y::B_FULL + u % NS], (u / NS) & 1, abort, err); };
+        auto full = [&](int u) { return sleep_wait<false>(&bars[Y::B_FULL + u % NS], (u / NS) & 1, abort, err); };
         auto kv = [&](int u) { return sb + Y::KV_OFF + (uint32_t)(u % NS) * Y::UNIT; };
         // S = Q K^T over one unit of K (all channels, or 128 of them)
         auto issue_qk = [&](int x, uint32_t dS, int u, int half) {
@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 bool ok = full(0);
                 for (int x = 0; x < 2 && ok; ++x) {
                     if (nblk[x] == 0) continue;
-                    ok = lane_wait(&bars[Y::B_Q + x], 0, abort, err);
+                    ok = sleep_wait<false>(&bars[Y::B_Q + x], 0, abort, err);
                     if (!ok) break;
                     tc_fence_after();
                     issue_qk(x, tmem + 128u * x, 0, 0);
@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     ok = full(uv);
                     for (int x = 0; x < 2 && ok; ++x) {
                         if (j >= nblk[x]) continue;
-                        ok = lane_wait(&bars[Y::B_P + x], j & 1, abort, err);
+                        ok = sleep_wait<false>(&bars[Y::B_P + x], j & 1, abort, err);
                         if (!ok) break;
                         tc_fence_after();
                         issue_pv(tmem + Y::TM_O + (uint32_t)(D * x), tmem + 128u * x, uv, 0, j == 0);
@@ -392,11 +392,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                     mma_commit(&bars[Y::B_S + (j & 1)]);
                     return true;
                 };
-                bool ok = lane_wait(&bars[Y::B_Q], 0, abort, err);
+                bool ok = sleep_wait<false>(&bars[Y::B_Q], 0, abort, err);
                 if (ok) ok = qk(0);
                 for (int j = 0; j < n && ok; ++j) {
                     if (j + 1 < n && !(ok = qk(j + 1))) break;
-                    ok = lane_wait(&bars[Y::B_P + (j & 1)], (j >> 1) & 1, abort, err);
+                    ok = sleep_wait<false>(&bars[Y::B_P + (j & 1)], (j >> 1) & 1, abort, err);
                     if (!ok) break;
                     const int u0 = (j == n - 1 ? 2 * n - 1 : 2 * j + 2) * NU;
                     for (int h = 0; h < NU && ok; ++h) {
@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         int wphase = 0;
         for (int j = 0; j < nb; ++j) {
             const uint32_t tS = tl + 128u * (DUAL ? x : (j & 1));
-            ok = warp_wait_u(&bars[Y::B_S + (DUAL ? x : (j & 1))], (DUAL ? j : (j >> 1)) & 1, abort, err);
+            ok = sleep_wait(&bars[Y::B_S + (DUAL ? x : (j & 1))], (DUAL ? j : (j >> 1)) & 1, abort, err);
             if (!ok) break;
             tc_fence_after();
             float s[NCOL];
@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 float *rb = red + (wphase & 1) * 256;
                 rb[wg * 128 + r] = mb;
                 warp_arrive(&bars[Y::B_WG]);
-                ok = warp_wait_u(&bars[Y::B_WG], wphase & 1, abort, err);
+                ok = sleep_wait(&bars[Y::B_WG], wphase & 1, abort, err);
                 ++wphase;
                 if (!ok) break;
                 mb = fmaxf(mb, rb[(wg ^ 1) * 128 + r]);
@@ -484,7 +484,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if constexpr (!DUAL) {
                         // the previous block's P.V must be complete (with two row
                         // tiles it is: S of this block was issued after it)
-                        ok = warp_wait(&bars[Y::B_O], (j - 1) & 1, abort, err);
+                        ok = sleep_wait(&bars[Y::B_O], (j - 1) & 1, abort, err);
                         if (!ok) break;
                         tc_fence_after();
                     }
@@ -532,7 +532,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 constexpr int NT = DUAL ? 128 : 256, KEYS = BN / NU;
                 for (int hf = 0; hf < NU && ok; ++hf) {
                     const int u = tt * NU + hf;
-                    ok = warp_wait_u(&bars[Y::B_FULL + u % NS], (u / NS) & 1, abort, err);
+                    ok = sleep_wait(&bars[Y::B_FULL + u % NS], (u / NS) & 1, abort, err);
                     if (!ok) break;
                     const int from = max(0, tail - hf * KEYS);
                     uint8_t *vt = smem + Y::KV_OFF + (u % NS) * Y::UNIT;
@@ -552,14 +552,14 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         // ---- output rows
         if (ok && nb > 0)
-            ok = DUAL ? warp_wait_u(&bars[Y::B_O + x], 0, abort, err)
-                      : warp_wait_u(&bars[Y::B_O], (nb - 1) & 1, abort, err);
+            ok = DUAL ? sleep_wait(&bars[Y::B_O + x], 0, abort, err)
+                      : sleep_wait(&bars[Y::B_O], (nb - 1) & 1, abort, err);
         if constexpr (!DUAL) {
             if (ok && nb > 0) {
                 float *rb = red + (wphase & 1) * 256;
                 rb[wg * 128 + r] = l;
                 warp_arrive(&bars[Y::B_WG]);
-                ok = warp_wait_u(&bars[Y::B_WG], wphase & 1, abort, err);
+                ok = sleep_wait(&bars[Y::B_WG], wphase & 1, abort, err);
                 if (ok) l = wg == 0 ? l + rb[128 + r] : rb[r] + l;
             }
         }

@@ -170,6 +170,43 @@ __device__ __forceinline__ bool lane_wait(uint64_t *bar, uint32_t parity, volati
     return ok;
 }
 
+// Waits that suspend the warp in hardware until the phase completes or 50 us
+// have passed, instead of polling: a polling warp takes issue slots and
+// shared-memory queue entries from the warps that compute (the sum over rows of
+// pa_mass_tc.cu ran several times slower beside pollers).
+__device__ __forceinline__ bool mbar_sleep_wait(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(50000u)
+        : "memory");
+    return ok != 0;
+}
+
+// Bounded wait of a whole warp (or, with WARP = false, of the calling thread alone)
+template <bool WARP = true>
+__device__ __forceinline__ bool sleep_wait(uint64_t *bar, uint32_t parity, volatile int *abort, uint32_t &err) {
+    auto done = [&](bool ok) { return WARP ? __all_sync(0xffffffffu, ok) != 0 : ok; };
+    if (done(mbar_try_wait(bar, parity))) return true;
+    const unsigned long long t0 = globaltimer();
+    while (true) {
+        if (done(mbar_sleep_wait(bar, parity))) return true;
+        const bool stop = *abort != 0 || globaltimer() - t0 > WAIT_LIMIT_NS;
+        if (WARP ? __any_sync(0xffffffffu, stop) != 0 : stop) {
+            if (WARP ? (threadIdx.x & 31) == 0 : true) {
+                if (*abort == 0) {
+                    *abort = 1;
+                    err |= PA_DEV_ERR_TIMEOUT;
+                }
+            }
+            return false;
+        }
+    }
+}
+
 __device__ __forceinline__ void warp_arrive(uint64_t *bar) {
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
