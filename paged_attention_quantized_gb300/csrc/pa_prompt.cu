@@ -45,6 +45,7 @@
 #include <atomic>
 #include <cmath>
 #include <mutex>
+#include <type_traits>
 
 #include "pa_attn.cuh"
 #include "pa_tc.cuh"
@@ -252,7 +253,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     int *misc = reinterpret_cast<int *>(smem + Y::MISC_OFF);
     volatile int *abort = misc + 1;
     float *red = reinterpret_cast<float *>(smem + Y::RED_OFF);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     const float NaN = __int_as_float(0x7fc00000);
     const int TQ = P.tpt * QT;
 
@@ -472,158 +473,178 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             __syncwarp();
         } else if (warp == W_MMA) {
-            // ================================================== MMA issue (lane 0 alone)
+            // ================================================== MMA issue
             constexpr uint32_t FMT = BF16 ? (1u << 7) | (1u << 10) : 0u;
             constexpr uint32_t ID_S = idesc(128, BN, 0) | FMT;
             constexpr uint32_t ID_O = idesc(128, D, 0) | FMT | (1u << 16);  // B = V read MN-major
-            auto full = [&](int u) { return sleep_wait<false>(&bars[Y::B_FULL + u % NS], (u / NS) & 1, abort, err); };
-            auto kv = [&](int u) { return sb + Y::KV_OFF + (uint32_t)(u % NS) * Y::UNIT; };
+            // The issuing warp is on the critical path (its waits and address arithmetic
+            // are not hidden by the tensor pipe's short queue): the ring
+            // position is a counter, descriptors are a base plus a multiple of it.
+            struct Pos {
+                int slot, par;  // ring slot, parity of its phase
+                __device__ __forceinline__ Pos next() const {
+                    const bool wrap = slot == NS - 1;
+                    Pos r;
+                    r.slot = wrap ? 0 : slot + 1;
+                    r.par = par ^ (wrap ? 1 : 0);
+                    return r;
+                }
+            };
+            auto full = [&](Pos p) { return sleep_wait(&bars[Y::B_FULL + p.slot], p.par, abort, err); };
+            auto freed = [&](Pos p) { mma_commit_w(&bars[Y::B_FREE + p.slot]); };
+            const uint64_t qd = sdesc(sb + Y::Q_OFF, 16, 1024, 2), kd = sdesc(sb + Y::KV_OFF, 16, 1024, 2),
+                           vd = sdesc(sb + Y::KV_OFF, BN / NU * 128, 1024, 2);
             // S = Q K^T over one unit of K (all channels, or 128 of them)
-            auto issue_qk = [&](int x, uint32_t dS, int u, int half) {
-                const uint64_t a = sdesc(sb + Y::Q_OFF + x * Y::Q_BYTES + half * 2 * 128 * 128, 16, 1024, 2);
-                const uint64_t b = sdesc(kv(u), 16, 1024, 2);
+            auto issue_qk = [&](int x, uint32_t dS, Pos p, int half) {
+                const uint64_t a = qd + (uint32_t)((x * Y::Q_BYTES + half * 2 * 128 * 128) >> 4);
+                const uint64_t b = kd + (uint32_t)(p.slot * (Y::UNIT >> 4));
                 constexpr int STEPS = D / 16 / NU;
 #pragma unroll
                 for (int k = 0; k < STEPS; ++k) {
                     const uint32_t o = (uint32_t)((k >> 2) * (128 * 128) + 32 * (k & 3)) >> 4;
-                    mma_f16(dS, a + o, b + o, ID_S, (half > 0 || k > 0) ? 1u : 0u);
+                    mma_f16_w(dS, a + o, b + o, ID_S, (half > 0 || k > 0) ? 1u : 0u);
                 }
             };
             // O += P V over one unit of V (128 or 64 keys)
-            auto issue_pv = [&](uint32_t dO, uint32_t aP, int u, int half, bool first) {
+            auto issue_pv = [&](uint32_t dO, uint32_t aP, Pos p, int half, bool first) {
                 constexpr int KEYS = BN / NU;
-                const uint64_t b = sdesc(kv(u), KEYS * 128, 1024, 2);
+                const uint64_t b = vd + (uint32_t)(p.slot * (Y::UNIT >> 4));
 #pragma unroll
                 for (int k = 0; k < KEYS / 16; ++k)
-                    mma_f16_ts(dO, aP + (uint32_t)(half * KEYS / 2 + 8 * k), b + (uint32_t)((k * 16 * 128) >> 4), ID_O,
+                    mma_f16_ts_w(dO, aP + (uint32_t)(half * KEYS / 2 + 8 * k), b + (uint32_t)((k * 16 * 128) >> 4), ID_O,
                                (!first || half > 0 || k > 0) ? 1u : 0u);
             };
-            if (lane == 0) {
+            {
                 bool ok = true;
                 int tok0, ntok;  // (not used here)
+                Pos pos;         // of the next unit
+                pos.slot = pos.par = 0;
                 if constexpr (DUAL) {
-                    // ring unit; per row tile x in bit x: parities of its tiles and blocks
-                    // so far, and whether it has had a tile
-                    int u = 0;
+                    // per row tile x in bit x: parities of its tiles and blocks so far, and
+                    // whether it has had a tile
                     uint32_t qpar = 0, ppar = 0, had = 0;
-                    // the first S of a tile's row tile x, from ring unit uk
-                    auto first_qk = [&](int x, int nx, int uk) {
+                    // the first S of a tile's row tile x, of nx blocks, from the K unit at p
+                    auto first_qk = [&](int x, int nx, Pos p, bool wait) {
                         if (nx == 0 || !ok) return;
-                        ok = sleep_wait<false>(&bars[Y::B_Q + x], (qpar >> x) & 1, abort, err) && full(uk);
+                        ok = (!wait || full(p)) && sleep_wait(&bars[Y::B_Q + x], (qpar >> x) & 1, abort, err);
                         if (!ok) return;
                         tc_fence_after();
-                        issue_qk(x, tmem + 128u * x, uk, 0);
-                        mma_commit(&bars[Y::B_S + x]);
-                        if (nx == 1) mma_commit(&bars[Y::B_QFREE + x]);
+                        issue_qk(x, tmem + 128u * x, p, 0);
+                        mma_commit_w(&bars[Y::B_S + x]);
+                        if (nx == 1) mma_commit_w(&bars[Y::B_QFREE + x]);
                     };
-                    Tile t = info(0, true);
-                    int n0 = rows_of(t, 0, tok0, ntok), n1 = rows_of(t, 1, tok0, ntok);
+                    Tile t = info(0, false);
+                    int n0 = uniform(rows_of(t, 0, tok0, ntok)), n1 = uniform(rows_of(t, 1, tok0, ntok));
                     if (max(n0, n1) > 0) {
-#pragma unroll 1
-                        for (int x = 0; x < 2; ++x) first_qk(x, x == 0 ? n0 : n1, 0);
-                        if (ok) mma_commit(&bars[Y::B_FREE + 0]);
+                        first_qk(0, n0, pos, true);
+                        first_qk(1, n1, pos, n0 == 0);
+                        if (ok) freed(pos);
                     }
                     for (int r = 0; ok && t.seq >= 0; ++r) {
                         const int n = max(n0, n1);
-                        // K0 of this tile is ring unit u; V(j) is u + 2j + 1, K(j + 1) u + 2j + 2,
-                        // and K0 of the next one u + 2n
-                        t = info(r + 1, true);
-                        const int m0 = rows_of(t, 0, tok0, ntok), m1 = rows_of(t, 1, tok0, ntok);
+                        // units of the tile: K0 (done), V0 K1 V1 K2 ... V(n-1), then K0 of the next one
+                        t = info(r + 1, false);
+                        const int m0 = uniform(rows_of(t, 0, tok0, ntok)), m1 = uniform(rows_of(t, 1, tok0, ntok));
                         const bool more = max(m0, m1) > 0;
                         if (n == 0 && more) {  // (a tile without keys)
-#pragma unroll 1
-                            for (int x = 0; x < 2; ++x) first_qk(x, x == 0 ? m0 : m1, u);
-                            if (ok) mma_commit(&bars[Y::B_FREE + u % NS]);
+                            first_qk(0, m0, pos, true);
+                            first_qk(1, m1, pos, m0 == 0);
+                            if (ok) freed(pos);
                         }
                         for (int j = 0; j < n && ok; ++j) {
-                            const int uv = u + 2 * j + 1, uk = uv + 1;
+                            const Pos pv = pos.next(), pk = pv.next();
                             const bool last = j == n - 1;
-#pragma unroll 1
-                            for (int x = 0; x < 2 && ok; ++x) {
+                            // row tile x: P.V of block j, S of block j + 1 (or of the next tile's first)
+                            auto step = [&](auto xc) {
+                                constexpr int x = decltype(xc)::value;
+                                if (!ok) return;
                                 const int nx = x == 0 ? n0 : n1;
                                 if (j < nx) {
-                                    ok = full(uv);
+                                    if (x == 0 || j >= n0) ok = full(pv);
                                     if (j == 0) {
                                         if ((had >> x) & 1)  // the output of the tile before has been read
-                                            ok = ok && sleep_wait<false>(&bars[Y::B_OFREE + x], ((qpar >> x) & 1) ^ 1, abort, err);
+                                            ok = ok && sleep_wait(&bars[Y::B_OFREE + x], ((qpar >> x) & 1) ^ 1, abort, err);
                                         had |= 1u << x;
                                         qpar ^= 1u << x;
                                     }
-                                    ok = ok && sleep_wait<false>(&bars[Y::B_P + x], (ppar >> x) & 1, abort, err);
-                                    if (!ok) break;
+                                    ok = ok && sleep_wait(&bars[Y::B_P + x], (ppar >> x) & 1, abort, err);
+                                    if (!ok) return;
                                     ppar ^= 1u << x;
                                     tc_fence_after();
-                                    issue_pv(tmem + Y::TM_O + (uint32_t)(D * x), tmem + 128u * x, uv, 0, j == 0);
-                                    if (j + 1 == nx) mma_commit(&bars[Y::B_O + x]);
+                                    issue_pv(tmem + Y::TM_O + (uint32_t)(D * x), tmem + 128u * x, pv, 0, j == 0);
+                                    if (j + 1 == nx) mma_commit_w(&bars[Y::B_O + x]);
                                 }
-                                if (x == 1) mma_commit(&bars[Y::B_FREE + uv % NS]);  // both row tiles are past V(j)
+                                if (x == 1) freed(pv);  // both row tiles are past V(j)
                                 if (!last) {
                                     if (j + 1 < nx) {
-                                        ok = full(uk);
-                                        if (!ok) break;
+                                        if (x == 0 || j + 1 >= n0) ok = full(pk);
+                                        if (!ok) return;
                                         tc_fence_after();
-                                        issue_qk(x, tmem + 128u * x, uk, 0);
-                                        mma_commit(&bars[Y::B_S + x]);
-                                        if (j + 2 == nx) mma_commit(&bars[Y::B_QFREE + x]);
+                                        issue_qk(x, tmem + 128u * x, pk, 0);
+                                        mma_commit_w(&bars[Y::B_S + x]);
+                                        if (j + 2 == nx) mma_commit_w(&bars[Y::B_QFREE + x]);
                                     }
                                 } else if (more) {
-                                    first_qk(x, x == 0 ? m0 : m1, uk);
+                                    first_qk(x, x == 0 ? m0 : m1, pk, x == 0 || m0 == 0);
                                 }
-                            }
-                            if (ok && (!last || more)) mma_commit(&bars[Y::B_FREE + uk % NS]);
+                            };
+                            step(std::integral_constant<int, 0>());
+                            step(std::integral_constant<int, 1>());
+                            if (ok && (!last || more)) freed(pk);
+                            pos = pk;
                         }
-                        u += 2 * n;
                         n0 = m0;
                         n1 = m1;
-                        mbar_arrive(&bars[Y::B_INFOFREE + r % NINFO]);
+                        warp_arrive(&bars[Y::B_INFOFREE + r % NINFO]);
                     }
                 } else {
-                    int u = 0, nt = 0, nb = 0;  // ring unit, tiles with keys and blocks so far
+                    int nt = 0, nb = 0;  // tiles with keys and blocks so far
                     for (int r = 0; ok; ++r) {
-                        const Tile t = info(r, true);
+                        const Tile t = info(r, false);
                         if (t.seq < 0) break;
-                        const int n = rows_of(t, 0, tok0, ntok);
-                        auto qk = [&](int j) -> bool {  // the tile's unit index: K0 = 0, K(j) = 2j - 1
-                            const int u0 = u + (j == 0 ? 0 : 2 * j - 1) * NU;
+                        const int n = uniform(rows_of(t, 0, tok0, ntok));
+                        auto qk = [&](int j) -> bool {  // units in order: K0 K1 V0 K2 V1 ... V(n-1)
+#pragma unroll
                             for (int h = 0; h < NU; ++h) {
-                                if (!full(u0 + h)) return false;
+                                if (!full(pos)) return false;
                                 tc_fence_after();
-                                issue_qk(0, tmem + 128u * ((nb + j) & 1), u0 + h, h);
-                                mma_commit(&bars[Y::B_FREE + (u0 + h) % NS]);
+                                issue_qk(0, tmem + 128u * ((nb + j) & 1), pos, h);
+                                freed(pos);
+                                pos = pos.next();
                             }
-                            mma_commit(&bars[Y::B_S + ((nb + j) & 1)]);
-                            if (j == n - 1) mma_commit(&bars[Y::B_QFREE]);
+                            mma_commit_w(&bars[Y::B_S + ((nb + j) & 1)]);
+                            if (j == n - 1) mma_commit_w(&bars[Y::B_QFREE]);
                             return true;
                         };
                         if (n > 0) {
-                            ok = sleep_wait<false>(&bars[Y::B_Q], nt & 1, abort, err);
+                            ok = sleep_wait(&bars[Y::B_Q], nt & 1, abort, err);
                             if (ok) ok = qk(0);
                             for (int j = 0; j < n && ok; ++j) {
                                 if (j + 1 < n && !(ok = qk(j + 1))) break;
                                 if (j == 0 && nt > 0)  // the output of the tile before has been read
-                                    ok = sleep_wait<false>(&bars[Y::B_OFREE], (nt - 1) & 1, abort, err);
+                                    ok = sleep_wait(&bars[Y::B_OFREE], (nt - 1) & 1, abort, err);
                                 const int b = nb + j;
-                                ok = ok && sleep_wait<false>(&bars[Y::B_P + (b & 1)], (b >> 1) & 1, abort, err);
+                                ok = ok && sleep_wait(&bars[Y::B_P + (b & 1)], (b >> 1) & 1, abort, err);
                                 if (!ok) break;
-                                const int u0 = u + (j == n - 1 ? 2 * n - 1 : 2 * j + 2) * NU;
-                                for (int h = 0; h < NU && ok; ++h) {
-                                    ok = full(u0 + h);
+#pragma unroll
+                                for (int h = 0; h < NU; ++h) {
+                                    ok = ok && full(pos);
                                     if (!ok) break;
                                     tc_fence_after();
-                                    issue_pv(tmem + Y::TM_O, tmem + 128u * (b & 1), u0 + h, h, j == 0);
-                                    mma_commit(&bars[Y::B_FREE + (u0 + h) % NS]);
+                                    issue_pv(tmem + Y::TM_O, tmem + 128u * (b & 1), pos, h, j == 0);
+                                    freed(pos);
+                                    pos = pos.next();
                                 }
-                                mma_commit(&bars[Y::B_O]);
+                                mma_commit_w(&bars[Y::B_O]);
                             }
                             ++nt;
                             nb += n;
-                            u += 2 * n * NU;
                         }
-                        mbar_arrive(&bars[Y::B_INFOFREE + r % NINFO]);
+                        warp_arrive(&bars[Y::B_INFOFREE + r % NINFO]);
                     }
                 }
-                mma_commit(&bars[Y::B_DONE]);
-                (void)mbar_wait_bounded(&bars[Y::B_DONE], 0, nullptr);
+                mma_commit_w(&bars[Y::B_DONE]);
+                if (lane == 0) (void)mbar_wait_bounded(&bars[Y::B_DONE], 0, nullptr);
             }
             __syncwarp();
         }

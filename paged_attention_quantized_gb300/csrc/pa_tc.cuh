@@ -180,6 +180,34 @@ __device__ __forceinline__ bool lane_wait(uint64_t *bar, uint32_t parity, volati
     return ok;
 }
 
+// The same instructions for a warp that runs its role whole (no branch on the
+// lane): one elected lane issues.  Control flow and descriptors then stay
+// warp-uniform, so that they live in uniform registers, which the instruction
+// takes; from a single-lane branch every operand is moved there first, some 30
+// to 40 cycles more per MMA (measured: 8 MMAs of M128 N48 K16 705 cycles, of
+// which 384 in the tensor pipe).
+__device__ __forceinline__ void mma_f16_w(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+    asm volatile("{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(id), "r"(acc));
+}
+
+__device__ __forceinline__ void mma_f16_ts_w(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t id, uint32_t acc) {
+    asm volatile("{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+                 "r"(a_tmem), "l"(b), "r"(id), "r"(acc));
+}
+
+__device__ __forceinline__ void mma_commit_w(uint64_t *bar) {
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+                 "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+                     smem_u32(bar))
+                 : "memory");
+}
+
+// a value that is the same in all lanes, as the compiler can see
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 // Waits that suspend the warp in hardware until the phase completes or 50 us
 // have passed, instead of polling: a polling warp takes issue slots and
 // shared-memory queue entries from the warps that compute (the sum over rows of
