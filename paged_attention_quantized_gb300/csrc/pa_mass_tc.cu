@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(mtc::THREADS, 1) pa_mass_tc_kernel(MassParams 
     int *misc = reinterpret_cast<int *>(smem + Y::MISC_OFF);
     volatile int *abort = misc + 1;
     int *ps = reinterpret_cast<int *>(smem + Y::PS_OFF);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     const float NaN = __int_as_float(0x7fc00000);
     if (sb & 1023) {
         if (tid == 0 && P.dev_error) atomicOr(P.dev_error, PA_DEV_ERR_TIMEOUT);
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(mtc::THREADS, 1) pa_mass_tc_kernel(MassParams 
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = (uint32_t)misc[0];
+    const uint32_t tmem = (uint32_t)uniform(misc[0]);
     uint32_t err = 0;
     Walk w;
     w.x = x0;
@@ -525,43 +525,50 @@ __global__ void __launch_bounds__(mtc::THREADS, 1) pa_mass_tc_kernel(MassParams 
         }
     } else {
         regs_dec<REGS_MMA>();
-        // ================================================== MMA issue (one thread)
-        if (warp == W_MMA && lane == 0) {
+        // ================================================== MMA issue (one warp)
+        if (warp == W_MMA) {
             const int rp = rows_c, n = nt * rp;
             const uint64_t qpanel = (uint64_t)(n * 128 >> 4);  // descriptor step between channel panels of the rows
             constexpr uint32_t FMT = BF ? (1u << 7) | (1u << 10) : 0u;
             const uint32_t id = idesc(CH, n, 0) | FMT;
-            int i = 0, seg = -1, pb = -1, pg = -1, pc = -1, pua = -1;
-            int used[2] = {0, 0};
-            for (; !w.end; ++i) {
-                if (w.b != pb || w.g != pg || w.c != pc || w.ua != pua) {
-                    ++seg;
-                    pb = w.b;
-                    pg = w.g;
-                    pc = w.c;
-                    pua = w.ua;
-                    if (!sleep_wait<false>(&bars[Y::B_QFULL], seg & 1, abort, err)) break;
+            const uint64_t ad = sdesc(sb + Y::A_OFF, 16, 1024, 2), qd = sdesc(sb + Y::Q_OFF, 16, 1024, 2);
+            int slot = 0, spar = 0, seg = 0;
+            uint32_t used = 0, bpar = 0;  // per S buffer: whether it was used, parity of its uses
+            bool ok = true;
+            for (; !w.end && ok; walk_piece(w, P, ps)) {
+                const int ua = uniform(w.ua), ue = uniform(w.ue);
+                for (int c = 0; c < chunks && ok; ++c, ++seg) {
+                    ok = sleep_wait(&bars[Y::B_QFULL], seg & 1, abort, err);
+                    for (int u = ua; u < ue && ok; ++u) {
+                        const int buf = u & 1;
+                        ok = sleep_wait(&bars[Y::B_AFULL + slot], spar, abort, err);
+                        // (the use before: one parity back)
+                        if (ok && ((used >> buf) & 1))
+                            ok = sleep_wait(&bars[Y::B_SFREE + buf], ((bpar >> buf) & 1) ^ 1, abort, err);
+                        if (!ok) break;
+                        used |= 1u << buf;
+                        bpar ^= 1u << buf;
+                        tc_fence_after();
+                        const uint64_t a = ad + (uint32_t)(slot * (Y::A_BYTES >> 4));
+                        uint64_t q = qd;
+                        const uint32_t d = tmem + 256u * buf;
+#pragma unroll
+                        for (int pn = 0; pn < D / 64; ++pn, q += qpanel)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                mma_f16_w(d, a + (uint32_t)((pn * CH * 128 + 32 * k) >> 4), q + 2u * k, id,
+                                          (pn > 0 || k > 0) ? 1u : 0u);
+                        mma_commit_w(&bars[Y::B_SFULL + buf]);
+                        mma_commit_w(&bars[Y::B_AFREE + slot]);
+                        const bool wrap = slot == NA - 1;
+                        slot = wrap ? 0 : slot + 1;
+                        spar ^= wrap ? 1 : 0;
+                    }
+                    if (ok) mma_commit_w(&bars[Y::B_QFREE]);
                 }
-                const int slot = i % NA, buf = w.u & 1;
-                if (!sleep_wait<false>(&bars[Y::B_AFULL + slot], (i / NA) & 1, abort, err)) break;
-                if (used[buf] > 0 && !sleep_wait<false>(&bars[Y::B_SFREE + buf], (used[buf] - 1) & 1, abort, err)) break;
-                ++used[buf];
-                tc_fence_after();
-                const uint64_t a = sdesc(sb + Y::A_OFF + slot * Y::A_BYTES, 16, 1024, 2);
-                uint64_t q = sdesc(sb + Y::Q_OFF, 16, 1024, 2);
-#pragma unroll
-                for (int pn = 0; pn < D / 64; ++pn, q += qpanel)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_f16(tmem + 256u * buf, a + (uint32_t)((pn * CH * 128 + 32 * k) >> 4), q + 2u * k, id,
-                                (pn > 0 || k > 0) ? 1u : 0u);
-                mma_commit(&bars[Y::B_SFULL + buf]);
-                mma_commit(&bars[Y::B_AFREE + slot]);
-                walk_next(w, P, ps, chunks);
-                if (w.end || w.b != pb || w.g != pg || w.c != pc || w.ua != pua) mma_commit(&bars[Y::B_QFREE]);
             }
-            mma_commit(&bars[Y::B_DONE]);
-            (void)mbar_wait_bounded(&bars[Y::B_DONE], 0, nullptr);
+            mma_commit_w(&bars[Y::B_DONE]);
+            if (lane == 0) (void)mbar_wait_bounded(&bars[Y::B_DONE], 0, nullptr);
         }
         __syncwarp();
     }

@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = (uint32_t)misc[0];
+    const uint32_t tmem = (uint32_t)uniform(misc[0]);
     uint32_t err = 0;
 
     // the r-th announced tile; its entry stays until every role has freed it
