@@ -1,8 +1,8 @@
 // Accumulated attention weight for many query rows per kv head, on the
 // fifth-generation tensor cores.
 //
-//   S^T = K q^T   M = 128 tokens, N = rows (times two for two-term queries),
-//                 K = head dim, f16 or bf16
+//   S^T = K q^T   M = 128 tokens, N = up to 256 rows, K = head dim (once per
+//                 term of the queries), f16 or bf16
 //   mass[t] += sum over rows of exp(c S^T[t, r] - lse_r)   t < vis_r
 //
 // The warp-level kernel (pa_mass.cu) keeps the query in registers, which
@@ -41,16 +41,12 @@ static_assert(512 * REGS_WORK + 128 * REGS_MMA <= THREADS * REGS_LAUNCH, "regist
 
 template <int D>
 struct Lay {
-    static constexpr int NA = D == 64 ? 4 : D == 128 ? 3 : 2;  // A buffers
-    static constexpr int NMAX = D == 256 ? 128 : 256;          // rows of the B operand (terms included)
-    static constexpr int PANELS = D / 64;
+    static constexpr int NA = D == 64 ? 4 : D == 128 ? 3 : 2;  // A buffers at most
+    static constexpr int RMAX = D == 256 ? 128 : 256;          // query rows of a chunk
     static constexpr int A_BYTES = CH * D * 2;
-    static constexpr int A_OFF = 0;
-    static constexpr int Q_OFF = NA * A_BYTES;
-    static constexpr int Q_BYTES = NMAX * D * 2;
-    static constexpr int CST_OFF = Q_OFF + Q_BYTES;            // [2 segments][128 pairs] {sc0, sc1, -ls0, -ls1}
-    static constexpr int VIS_OFF = CST_OFF + 2 * (NMAX / 2) * 16;  // [2][NMAX]
-    static constexpr int BAR_OFF = VIS_OFF + 2 * NMAX * 4;
+    static constexpr int CST_OFF = 0;                          // [2 segments][RMAX / 2 pairs] {sc0, sc1, -lse0, -lse1}
+    static constexpr int VIS_OFF = CST_OFF + 2 * (RMAX / 2) * 16;  // [2][RMAX]
+    static constexpr int BAR_OFF = VIS_OFF + 2 * RMAX * 4;
     enum {
         B_AFULL = 0,              // [NA] tile in place
         B_AFREE = B_AFULL + NA,   // [NA] its MMAs complete
@@ -62,7 +58,9 @@ struct Lay {
         NBARS = B_DONE + 1
     };
     static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;  // [0] tmem, [1] abort, [2] errors, [4 ..] scan
-    static constexpr int PS_OFF = MISC_OFF + 128;         // prefix sums (B + 1 ints)
+    static constexpr int A_OFF = (MISC_OFF + 128 + 1023) / 1024 * 1024;
+    // then the A buffers, the query operand and the prefix sums (B + 1 ints)
+    static constexpr int ROOM = 227 * 1024 - A_OFF - (MAX_B + 1) * 4;
 };
 
 // the CTA's tiles: pieces of one (request, kv head), each walked once per chunk of rows
@@ -105,22 +103,19 @@ __device__ __forceinline__ uint32_t op_off(int rows, int t, int c) {
 
 // the sum over rows of a tile that some row does not see all of (the last
 // ones of a request): rows taken two by two, each against its visible length
-__device__ __noinline__ float masked_sum(uint32_t tl, int rp, int nt, const float *cst, const int *vs, int tok,
-                                         float ts) {
+__device__ __noinline__ float masked_sum(uint32_t tl, int rp, const float *cst, const int *vs, int tok, float ts) {
     float tot = 0.f;
 #pragma unroll 1
     for (int r0 = 0; r0 < rp; r0 += 8) {
-        uint32_t z[8], z2[8];
+        uint32_t z[8];
         tmem_ld8_nowait(tl + (uint32_t)r0, z);
-        if (nt == 2) tmem_ld8_nowait(tl + (uint32_t)(rp + r0), z2);
         tmem_ld_wait();
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             float d = __uint_as_float(z[e]);
-            if (nt == 2) d += __uint_as_float(z2[e]);
             const int r = r0 + e;
             d = fmaf(d * ts, cst[(r >> 1) * 4 + (r & 1)], cst[(r >> 1) * 4 + 2 + (r & 1)]);
-            if (tok < vs[r]) tot += ex2(d * LOG2E);
+            if (tok < vs[r]) tot += ex2(d);
         }
     }
     return tot;
@@ -129,19 +124,19 @@ __device__ __noinline__ float masked_sum(uint32_t tl, int rp, int nt, const floa
 }  // namespace mtc
 
 template <int D, int KV>
-__global__ void __launch_bounds__(mtc::THREADS, 1) pa_mass_tc_kernel(MassParams P, int nt, int rows_c, int chunks) {
+__global__ void __launch_bounds__(mtc::THREADS, 1) pa_mass_tc_kernel(MassParams P, int nt, int rows_c, int chunks, int na) {
     using namespace mtc;
     using Y = Lay<D>;
     constexpr int BITS = KV == PA_INT4 ? 4 : (KV == PA_E4M3 || KV == PA_INT8) ? 8 : 16;
     constexpr bool BF = KV == PA_BF16;
-    constexpr int NA = Y::NA;
+    const int NA = na, q_off = Y::A_OFF + na * Y::A_BYTES;  // A buffers; the query operand behind them
     constexpr int RB = D * BITS / 8, PR = RB / 16;  // bytes and 16-byte pieces per token
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sb = smem_u32(smem);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Y::BAR_OFF);
     int *misc = reinterpret_cast<int *>(smem + Y::MISC_OFF);
     volatile int *abort = misc + 1;
-    int *ps = reinterpret_cast<int *>(smem + Y::PS_OFF);
+    int *ps = reinterpret_cast<int *>(smem + q_off + nt * rows_c * D * 2);
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     const float NaN = __int_as_float(0x7fc00000);
     if (sb & 1023) {
@@ -157,7 +152,7 @@ __global__ void __launch_bounds__(mtc::THREADS, 1) pa_mass_tc_kernel(MassParams 
     if (tid == 0) {
         for (int i = 0; i < Y::NBARS; ++i) {
             uint32_t c = 1;
-            if ((i >= Y::B_AFULL && i < Y::B_AFULL + NA) || (i >= Y::B_SFREE && i < Y::B_SFREE + 2)) c = 4;
+            if ((i >= Y::B_AFULL && i < Y::B_AFULL + Y::NA) || (i >= Y::B_SFREE && i < Y::B_SFREE + 2)) c = 4;
             if (i == Y::B_QFULL) c = 8;
             mbar_init(&bars[i], c);
         }
@@ -186,6 +181,17 @@ __global__ void __launch_bounds__(mtc::THREADS, 1) pa_mass_tc_kernel(MassParams 
         // ================================================== loaders: tile i by warpgroup i & 1
         const int wg = warp >> 2, wq = warp & 3;  // the warp's 32 tokens: 32 wq ..
         int i = wg;                               // the next tile to publish
+        struct Slot {
+            int slot, par;  // buffer, parity of its uses
+        };
+        Slot put = {wg, 0};
+        auto two_on = [&](Slot a) -> Slot {
+            Slot b;
+            const bool wrap = a.slot + 2 >= NA;
+            b.slot = wrap ? a.slot + 2 - NA : a.slot + 2;
+            b.par = a.par ^ (wrap ? 1 : 0);
+            return b;
+        };
         // The warp's 32 tokens are two runs of 16 rows, each contiguous in its
         // block.  Their places are known QD tiles of this warpgroup ahead, so that
         // the block ids have arrived when the rows are asked for.
@@ -233,13 +239,13 @@ __global__ void __launch_bounds__(mtc::THREADS, 1) pa_mass_tc_kernel(MassParams 
         };
         if constexpr (BITS == 16) {
             // up to PF tiles of this warpgroup in flight, then publish the oldest
-            constexpr int PF = NA > 2 ? 2 : 1;
-            int ai = wg;  // the next tile to copy
+            const int PF = NA > 2 ? 2 : 1;
+            int ai = wg;          // the next tile to copy
+            Slot at = {wg, 0};    // its buffer
             while (i < mine) {
                 if (ai < mine && ai - i < 2 * PF) {
-                    const int slot = ai % NA;
-                    if (ai >= NA && !sleep_wait(&bars[Y::B_AFREE + slot], (ai / NA - 1) & 1, abort, err)) break;
-                    const uint32_t dst = sb + Y::A_OFF + slot * Y::A_BYTES;
+                    if (ai >= NA && !sleep_wait(&bars[Y::B_AFREE + at.slot], at.par ^ 1, abort, err)) break;
+                    const uint32_t dst = sb + Y::A_OFF + at.slot * Y::A_BYTES;
                     const int left = pl[0].left;
                     runs_of(pl[0]);
 #pragma unroll 4
@@ -251,13 +257,15 @@ __global__ void __launch_bounds__(mtc::THREADS, 1) pa_mass_tc_kernel(MassParams 
                     }
                     asm volatile("cp.async.commit_group;" ::: "memory");
                     ai += 2;
+                    at = two_on(at);
                     rotate();
                     if (ai < mine && ai - i < 2 * PF) continue;
                 }
                 if (ai - i > 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
                 else asm volatile("cp.async.wait_group 0;" ::: "memory");
                 fence_proxy_async_smem();
-                warp_arrive(&bars[Y::B_AFULL + i % NA]);
+                warp_arrive(&bars[Y::B_AFULL + put.slot]);
+                put = two_on(put);
                 i += 2;
             }
             asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -274,9 +282,9 @@ __global__ void __launch_bounds__(mtc::THREADS, 1) pa_mass_tc_kernel(MassParams 
                 }
             };
             fetch();
-            for (; i < mine; i += 2) {
-                const int slot = i % NA;
-                if (i >= NA && !sleep_wait(&bars[Y::B_AFREE + slot], (i / NA - 1) & 1, abort, err)) break;
+            for (; i < mine; i += 2, put = two_on(put)) {
+                const int slot = put.slot;
+                if (i >= NA && !sleep_wait(&bars[Y::B_AFREE + slot], put.par ^ 1, abort, err)) break;
                 uint8_t *dst = smem + Y::A_OFF + slot * Y::A_BYTES;
                 constexpr int OC = 16 / BITS;  // 16-byte operand chunks per raw piece
 #pragma unroll
@@ -301,12 +309,11 @@ __global__ void __launch_bounds__(mtc::THREADS, 1) pa_mass_tc_kernel(MassParams 
         const int wg = (warp - W_EPI) >> 2, qd = warp & 3;
         const int t = 32 * qd + lane;
         const uint32_t tl = tmem + ((uint32_t)(32 * qd) << 16) + 256u * wg;
-        const int rp = rows_c;  // rows of a term in the B operand
+        const int rp = rows_c;  // rows of the B operand
         int seg = -1, sphase = 0;
         bool ok = true;
         int f_blk = 0;
         float f_old = 0.f;
-        const uint64_t l2e = f2(LOG2E, LOG2E);
         for (; !w.end && ok; walk_piece(w, P, ps)) {
             const int u1 = w.ua + ((w.ua ^ wg) & 1);  // this warpgroup's first tile of the piece
             const int32_t *table = P.block_table + (size_t)w.b * P.tbl;
@@ -328,8 +335,8 @@ __global__ void __launch_bounds__(mtc::THREADS, 1) pa_mass_tc_kernel(MassParams 
                     ok = false;
                     break;
                 }
-                float *cst = reinterpret_cast<float *>(smem + Y::CST_OFF) + (seg & 1) * (Y::NMAX / 2) * 4;
-                int *vs = reinterpret_cast<int *>(smem + Y::VIS_OFF) + (seg & 1) * Y::NMAX;
+                float *cst = reinterpret_cast<float *>(smem + Y::CST_OFF) + (seg & 1) * (Y::RMAX / 2) * 4;
+                int *vs = reinterpret_cast<int *>(smem + Y::VIS_OFF) + (seg & 1) * Y::RMAX;
                 const float *fold = P.k_mode == PA_SCALE_CHANNEL ? P.k_scale + (size_t)w.g * D : nullptr;
                 const bool scaled = !BF && (fold != nullptr || P.q_dtype == PA_BF16);
                 constexpr int WP = 64 / BITS;  // operand words per raw piece
@@ -412,8 +419,8 @@ __global__ void __launch_bounds__(mtc::THREADS, 1) pa_mass_tc_kernel(MassParams 
                             float a = f.x * up, d = f.y * up;
                             for (int q = 0; q < nt; ++q) {
                                 const uint32_t x = pack2<BF>(a, d);
-                                *reinterpret_cast<uint32_t *>(smem + Y::Q_OFF + op_off(nt * rp, q * rp + rr0 + i, c) +
-                                                              4 * (word & 3)) = x;
+                                *reinterpret_cast<uint32_t *>(smem + q_off + q * rp * D * 2 +
+                                                              op_off(rp, rr0 + i, c) + 4 * (word & 3)) = x;
                                 if constexpr (BF) {
                                     a -= __uint_as_float(x << 16);
                                     d -= __uint_as_float(x & 0xFFFF0000u);
@@ -429,8 +436,10 @@ __global__ void __launch_bounds__(mtc::THREADS, 1) pa_mass_tc_kernel(MassParams 
                         const int rr = rr0 + lane;
                         const float ks = P.k_mode == PA_SCALE_TENSOR ? P.k_scale[0] : 1.f;
                         const bool on = lse != -INFINITY;
-                        cst[(rr >> 1) * 4 + (rr & 1)] = on ? P.softmax_scale * ks * my_down : 0.f;
-                        cst[(rr >> 1) * 4 + 2 + (rr & 1)] = on ? -lse : -INFINITY;
+                        // in the exp2 domain: the two roundings by log2 e cost some 2^-24 of a
+                        // score or of lse, as much as fp32 scores have anyway
+                        cst[(rr >> 1) * 4 + (rr & 1)] = on ? P.softmax_scale * ks * my_down * LOG2E : 0.f;
+                        cst[(rr >> 1) * 4 + 2 + (rr & 1)] = on ? -lse * LOG2E : -INFINITY;
                         vs[rr] = (vis != 0x7FFFFFFF && !on) ? 0 : vis;
                     }
                 }
@@ -462,26 +471,22 @@ __global__ void __launch_bounds__(mtc::THREADS, 1) pa_mass_tc_kernel(MassParams 
                     tc_fence_after();
                     const uint64_t ts2 = f2(ts, ts);
                     uint64_t tot[2] = {0, 0};
-                    auto add_rows = [&](auto ncol, auto terms, int r0) {
-                        constexpr int C = decltype(ncol)::value, NT = decltype(terms)::value;
-                        float z[C], z2[NT == 2 ? C : 1];
+                    auto add_rows = [&](auto ncol, int r0) {
+                        constexpr int C = decltype(ncol)::value;
+                        float z[C];
                         if constexpr (C == 32) {
                             tmem_ld32_nowait(tl + (uint32_t)r0, z);
                             tmem_wait32(z);
                         } else {
                             tmem_ld16_nowait(tl + (uint32_t)r0, reinterpret_cast<uint32_t *>(z));
-                            if constexpr (NT == 2)
-                                tmem_ld16_nowait(tl + (uint32_t)(rp + r0), reinterpret_cast<uint32_t *>(z2));
                             tmem_wait16(z);
-                            if constexpr (NT == 2) tmem_wait16(z2);
                         }
 #pragma unroll
                         for (int e = 0; e < C; e += 2) {
                             const ulonglong2 c = cst2[(r0 + e) >> 1];  // {scales, -lse} of two rows
                             uint64_t d = f2(z[e], z[e + 1]);
-                            if constexpr (NT == 2) d = add2(d, f2(z2[e], z2[e + 1]));
                             if (KV == PA_E4M3) d = mul2(d, ts2);
-                            d = mul2(fma2(d, c.x, c.y), l2e);
+                            d = fma2(d, c.x, c.y);
                             float a, b;
                             f2_split(d, a, b);
                             tot[(e >> 1) & 1] = add2(tot[(e >> 1) & 1], f2(ex2(a), ex2(b)));
@@ -489,19 +494,12 @@ __global__ void __launch_bounds__(mtc::THREADS, 1) pa_mass_tc_kernel(MassParams 
                     };
                     float got = 0.f;
                     if (masked) {
-                        got = masked_sum(tl, rp, nt, cst, vs, tok, ts);
+                        got = masked_sum(tl, rp, cst, vs, tok, ts);
                     } else {
-                        using I16 = std::integral_constant<int, 16>;
-                        using I1 = std::integral_constant<int, 1>;
                         int r0 = 0;
-                        if (nt == 2) {
 #pragma unroll 1
-                            for (; r0 < rp; r0 += 16) add_rows(I16(), std::integral_constant<int, 2>(), r0);
-                        } else {
-#pragma unroll 1
-                            for (; r0 + 32 <= rp; r0 += 32) add_rows(std::integral_constant<int, 32>(), I1(), r0);
-                            if (r0 < rp) add_rows(I16(), I1(), r0);
-                        }
+                        for (; r0 + 32 <= rp; r0 += 32) add_rows(std::integral_constant<int, 32>(), r0);
+                        if (r0 < rp) add_rows(std::integral_constant<int, 16>(), r0);
                         float a, b;
                         f2_split(add2(tot[0], tot[1]), a, b);
                         got = a + b;
@@ -527,11 +525,10 @@ __global__ void __launch_bounds__(mtc::THREADS, 1) pa_mass_tc_kernel(MassParams 
         regs_dec<REGS_MMA>();
         // ================================================== MMA issue (one warp)
         if (warp == W_MMA) {
-            const int rp = rows_c, n = nt * rp;
-            const uint64_t qpanel = (uint64_t)(n * 128 >> 4);  // descriptor step between channel panels of the rows
+            const uint64_t qpanel = (uint64_t)(rows_c * 128 >> 4);  // descriptor step between channel panels of the rows
             constexpr uint32_t FMT = BF ? (1u << 7) | (1u << 10) : 0u;
-            const uint32_t id = idesc(CH, n, 0) | FMT;
-            const uint64_t ad = sdesc(sb + Y::A_OFF, 16, 1024, 2), qd = sdesc(sb + Y::Q_OFF, 16, 1024, 2);
+            const uint32_t id = idesc(CH, rows_c, 0) | FMT;
+            const uint64_t ad = sdesc(sb + Y::A_OFF, 16, 1024, 2), qd = sdesc(sb + q_off, 16, 1024, 2);
             int slot = 0, spar = 0, seg = 0;
             uint32_t used = 0, bpar = 0;  // per S buffer: whether it was used, parity of its uses
             bool ok = true;
@@ -552,12 +549,14 @@ __global__ void __launch_bounds__(mtc::THREADS, 1) pa_mass_tc_kernel(MassParams 
                         const uint64_t a = ad + (uint32_t)(slot * (Y::A_BYTES >> 4));
                         uint64_t q = qd;
                         const uint32_t d = tmem + 256u * buf;
+                        // the terms of a query one after the other, into the same sums
+                        for (int t = 0; t < nt; ++t)
 #pragma unroll
-                        for (int pn = 0; pn < D / 64; ++pn, q += qpanel)
+                            for (int pn = 0; pn < D / 64; ++pn, q += qpanel)
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                mma_f16_w(d, a + (uint32_t)((pn * CH * 128 + 32 * k) >> 4), q + 2u * k, id,
-                                          (pn > 0 || k > 0) ? 1u : 0u);
+                                for (int k = 0; k < 4; ++k)
+                                    mma_f16_w(d, a + (uint32_t)((pn * CH * 128 + 32 * k) >> 4), q + 2u * k, id,
+                                              (t > 0 || pn > 0 || k > 0) ? 1u : 0u);
                         mma_commit_w(&bars[Y::B_SFULL + buf]);
                         mma_commit_w(&bars[Y::B_AFREE + slot]);
                         const bool wrap = slot == NA - 1;
@@ -584,8 +583,6 @@ __global__ void __launch_bounds__(mtc::THREADS, 1) pa_mass_tc_kernel(MassParams 
 template <int D, int KV>
 cudaError_t launch_tc(const MassParams &P, int nt, int sms, cudaStream_t s) {
     using Y = mtc::Lay<D>;
-    const int smem = Y::PS_OFF + (P.B + 1) * 4;
-    if (smem > 227 * 1024) return cudaErrorInvalidValue;
     static std::atomic<unsigned long long> done{0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -601,14 +598,19 @@ cudaError_t launch_tc(const MassParams &P, int nt, int sms, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         done.fetch_or(bit, std::memory_order_relaxed);
     }
-    // chunks of rows of equal size, as few as fit the operand
-    const int most = Y::NMAX / nt, chunks = (P.R + most - 1) / most;
-    int rows_c = (P.R + chunks - 1) / chunks;
-    rows_c = (rows_c + 15) / 16 * 16;  // (a multiple of the MMA's N step, also with two terms side by side)
+    // chunks of rows of equal size, as few as fit the operand beside two A buffers; then as many A buffers as fit
+    const int row_bytes = D * 2 * nt;
+    const int most = std::min((int)Y::RMAX, (Y::ROOM - 2 * Y::A_BYTES) / row_bytes / 16 * 16);
+    int chunks = (P.R + most - 1) / most;
+    // (multiples of the MMA's N step)
+    const int rows_c = ((P.R + chunks - 1) / chunks + 15) / 16 * 16;
+    chunks = (P.R + rows_c - 1) / rows_c;
+    const int na = std::min((int)Y::NA, (Y::ROOM - rows_c * row_bytes) / Y::A_BYTES);
+    const int smem = Y::A_OFF + na * Y::A_BYTES + rows_c * row_bytes + (P.B + 1) * 4;
     // no CTA without a tile of the longest possible batch
     const long long tiles = (long long)P.B * P.Hkv * ((P.max_ctx + mtc::CH - 1) / mtc::CH);
     const int ctas = (int)std::max(1ll, std::min<long long>(sms, tiles));
-    pa_mass_tc_kernel<D, KV><<<ctas, mtc::THREADS, smem, s>>>(P, nt, rows_c, (P.R + rows_c - 1) / rows_c);
+    pa_mass_tc_kernel<D, KV><<<ctas, mtc::THREADS, smem, s>>>(P, nt, rows_c, chunks, na);
     return cudaPeekAtLastError();
 }
 
