@@ -224,6 +224,12 @@ __global__ void __launch_bounds__(mtc::THREADS, 1) pa_mass_tc_kernel(MassParams 
             place(pl[QD - 1]);
         };
         const int mine = (int)(x1 - x0) * chunks;  // tiles of the CTA, all passes
+#ifdef PA_FAULT_INJECT
+        // tile (word >> 8) - 1 of CTA 0 is never published
+        const int fi = P.dev_error && blockIdx.x == 0 ? (int)(*P.dev_error >> 8) - 1 : -1;
+#else
+        constexpr int fi = -1;
+#endif
         const uint8_t *run[2];
         auto runs_of = [&](const Place &q) {
 #pragma unroll
@@ -264,7 +270,7 @@ __global__ void __launch_bounds__(mtc::THREADS, 1) pa_mass_tc_kernel(MassParams 
                 if (ai - i > 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
                 else asm volatile("cp.async.wait_group 0;" ::: "memory");
                 fence_proxy_async_smem();
-                warp_arrive(&bars[Y::B_AFULL + put.slot]);
+                if (i != fi) warp_arrive(&bars[Y::B_AFULL + put.slot]);
                 put = two_on(put);
                 i += 2;
             }
@@ -298,7 +304,7 @@ __global__ void __launch_bounds__(mtc::THREADS, 1) pa_mass_tc_kernel(MassParams 
                             make_uint4(wd[4 * o], wd[4 * o + 1], wd[4 * o + 2], wd[4 * o + 3]);
                 }
                 fence_proxy_async_smem();
-                warp_arrive(&bars[Y::B_AFULL + slot]);
+                if (i != fi) warp_arrive(&bars[Y::B_AFULL + slot]);
                 rotate();
                 fetch();  // the next tile of this warpgroup, while this one is used
             }
