@@ -12,7 +12,7 @@
 // s below `left` is s less the kept ones before it, that of a kept slot at or
 // past `left` is the kept ones between; the i-th of both pair up as the moves.
 //
-// Moves (pa_evict_move_kernel): one thread per 16-byte piece of a moved K or V
+// Moves (pa_evict_move_kernel, or the selecting CTA when they are few): one thread per 16-byte piece of a moved K or V
 // row.  Sources lie at or past `left`, destinations below it, so no row is
 // read after it was written, whatever the order; HBM bound.
 #include <algorithm>
@@ -80,14 +80,90 @@ __device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t *s_warp, uin
     return before + x - v;
 }
 
+// Rows i0 .. i0 + MOVE_ROWS - 1 of the moves of row `rowi` = (b, g), by THREADS
+// threads; s_at: MOVE_ROWS x 4 entries of shared memory.  Sources lie at or past
+// `left` and destinations below it, so the order does not matter.
+template <int THREADS>
+__device__ __forceinline__ void move_chunk(const EvictParams &P, int b, int g, size_t rowi, int i0, int n,
+                                           long long (*s_at)[4]) {
+    const int tid = threadIdx.x, rows = min(MOVE_ROWS, n - i0);
+    const int32_t *dst = P.lists + rowi * 2 * P.cap + i0, *src = dst + P.cap;
+    const int32_t *table = P.block_table + (size_t)b * P.tbl;
+    for (int i = tid; i < rows; i += THREADS) {
+        const int s = src[i], d = dst[i];
+        const int bs_ = table[s / P.bs], bd = table[d / P.bs];
+        const long long rs = (long long)g * P.bs + s % P.bs, rd = (long long)g * P.bs + d % P.bs;
+        s_at[i][0] = (long long)bs_ * P.k_block + rs * P.k_row;
+        s_at[i][1] = (long long)bd * P.k_block + rd * P.k_row;
+        s_at[i][2] = (long long)bs_ * P.v_block + rs * P.v_row;
+        s_at[i][3] = (long long)bd * P.v_block + rd * P.v_row;
+        if (P.k_tok)
+            *reinterpret_cast<float *>(P.k_pool + (long long)bd * P.k_block + P.k_codes + rd * 4) =
+                *reinterpret_cast<const float *>(P.k_pool + (long long)bs_ * P.k_block + P.k_codes + rs * 4);
+        if (P.v_tok)
+            *reinterpret_cast<float *>(P.v_pool + (long long)bd * P.v_block + P.v_codes + rd * 4) =
+                *reinterpret_cast<const float *>(P.v_pool + (long long)bs_ * P.v_block + P.v_codes + rs * 4);
+    }
+    __syncthreads();
+    const int kp = P.k_row / 16, pieces = kp + P.v_row / 16;
+    const int dr = THREADS / pieces, dp = THREADS - dr * pieces;
+    int r = tid / pieces, p = tid - r * pieces;
+    constexpr int UN = 4;
+    while (r < rows) {
+        uint4 v[UN];
+        uint4 *to[UN];
+#pragma unroll
+        for (int q = 0; q < UN; ++q) {
+            to[q] = nullptr;
+            if (r < rows) {
+                const bool isk = p < kp;
+                uint8_t *pool = isk ? P.k_pool : P.v_pool;
+                const int o = 16 * (isk ? p : p - kp);
+                v[q] = *reinterpret_cast<const uint4 *>(pool + s_at[r][isk ? 0 : 2] + o);
+                to[q] = reinterpret_cast<uint4 *>(pool + s_at[r][isk ? 1 : 3] + o);
+            }
+            r += dr;
+            p += dp;
+            if (p >= pieces) {
+                p -= pieces;
+                ++r;
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < UN; ++q)
+            if (to[q]) *to[q] = v[q];
+    }
+}
+
+// Lengths and histories of the requests, and the error word
+__device__ __forceinline__ void finish(const EvictParams &P) {
+    __shared__ uint32_t s_e;
+    if (threadIdx.x == 0) s_e = 0;
+    __syncthreads();
+    uint32_t e = 0;
+    for (int b = threadIdx.x; b < P.B; b += blockDim.x) {
+        const int4 r = P.req[b];
+        P.lens_out[b] = r.x;
+        P.history_out[2 * b] = r.y;
+        P.history_out[2 * b + 1] = r.z;
+        e |= (uint32_t)r.w;
+    }
+    if (e) atomicOr(&s_e, e);
+    __syncthreads();
+    if (threadIdx.x == 0) P.hdr[0] = s_e;
+}
+
 // KPT: slots per thread kept in registers (slot i * THREADS + thread), 0 = read again each time
-template <int THREADS, int KPT>
+// FUSED: the CTA moves its rows as well
+template <int THREADS, int KPT, bool FUSED>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) pa_evict_select_kernel(EvictParams P) {
     constexpr int NW = THREADS / 32;
     grid_dependents_launch();  // the move kernel may queue up behind
     constexpr int BINS = 2048, BPT = BINS / THREADS;
     extern __shared__ uint32_t s_map[];  // one bit per slot, 32 consecutive slots a word; then the kept ones before each word
-    __shared__ int s_hist[BINS], s_n, s_bin, s_over, s_in;
+    __shared__ __align__(16) int s_hist[BINS];
+    __shared__ int s_n, s_bin, s_over, s_in;
+    static_assert(sizeof(s_hist) >= MOVE_ROWS * 32, "the moves' places use the histogram's room");
     __shared__ uint64_t s_warp[NW];
     __shared__ uint32_t s_few[32], s_pick, s_err;
     __shared__ int s_cut;
@@ -318,81 +394,45 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) pa_evict_select_kerne
     }
     __syncthreads();  // mass may be mass_out: the tail is cleared after its last read
     for (int s = left + tid; s < L; s += THREADS) mass_out[s] = 0.f;
-    if (tid == 0) P.counts[rowi] = moves;
+    if constexpr (FUSED) {
+        for (int i0 = 0; i0 < moves; i0 += MOVE_ROWS) {
+            move_chunk<THREADS>(P, b, g, rowi, i0, moves, reinterpret_cast<long long (*)[4]>(s_hist));
+            __syncthreads();
+        }
+    } else {
+        if (tid == 0) P.counts[rowi] = moves;
+    }
 }
 
 __global__ void __launch_bounds__(MOVE_THREADS) pa_evict_move_kernel(EvictParams P) {
-    grid_dependency_wait();
-    const int g = blockIdx.y % P.Hkv, b = blockIdx.y / P.Hkv;
-    const size_t rowi = blockIdx.y;
-    const int tid = threadIdx.x;
-    if (blockIdx.x == 0 && g == 0 && tid == 0) {
-        const int4 r = P.req[b];
-        P.lens_out[b] = r.x;
-        P.history_out[2 * b] = r.y;
-        P.history_out[2 * b + 1] = r.z;
-    }
-    if (blockIdx.x == 0 && blockIdx.y == 0) {
-        uint32_t e = 0;
-        for (int i = tid; i < P.B; i += MOVE_THREADS) e |= (uint32_t)P.req[i].w;
-        e = __reduce_or_sync(0xffffffffu, e);
-        __shared__ uint32_t s_e;
-        if (tid == 0) s_e = 0;
-        __syncthreads();
-        if ((tid & 31) == 0 && e) atomicOr(&s_e, e);
-        __syncthreads();
-        if (tid == 0) P.hdr[0] = s_e;
-    }
-    const int n = P.counts[rowi], i0 = blockIdx.x * MOVE_ROWS;
-    if (i0 >= n) return;
-    const int rows = min(MOVE_ROWS, n - i0);
-    const int32_t *dst = P.lists + rowi * 2 * P.cap + i0, *src = dst + P.cap;
-    const int32_t *table = P.block_table + (size_t)b * P.tbl;
     __shared__ long long s_at[MOVE_ROWS][4];  // K source, K destination, V source, V destination
-    if (tid < rows) {
-        const int s = src[tid], d = dst[tid];
-        const int bs_ = table[s / P.bs], bd = table[d / P.bs];
-        const long long rs = (long long)g * P.bs + s % P.bs, rd = (long long)g * P.bs + d % P.bs;
-        s_at[tid][0] = (long long)bs_ * P.k_block + rs * P.k_row;
-        s_at[tid][1] = (long long)bd * P.k_block + rd * P.k_row;
-        s_at[tid][2] = (long long)bs_ * P.v_block + rs * P.v_row;
-        s_at[tid][3] = (long long)bd * P.v_block + rd * P.v_row;
-        if (P.k_tok)
-            *reinterpret_cast<float *>(P.k_pool + (long long)bd * P.k_block + P.k_codes + rd * 4) =
-                *reinterpret_cast<const float *>(P.k_pool + (long long)bs_ * P.k_block + P.k_codes + rs * 4);
-        if (P.v_tok)
-            *reinterpret_cast<float *>(P.v_pool + (long long)bd * P.v_block + P.v_codes + rd * 4) =
-                *reinterpret_cast<const float *>(P.v_pool + (long long)bs_ * P.v_block + P.v_codes + rs * 4);
-    }
-    __syncthreads();
-    const int kp = P.k_row / 16, pieces = kp + P.v_row / 16;
-    const int dr = MOVE_THREADS / pieces, dp = MOVE_THREADS - dr * pieces;
-    int r = tid / pieces, p = tid - r * pieces;
-    constexpr int UN = 4;
-    while (r < rows) {
-        uint4 v[UN];
-        uint4 *to[UN];
-#pragma unroll
-        for (int q = 0; q < UN; ++q) {
-            to[q] = nullptr;
-            if (r < rows) {
-                const bool isk = p < kp;
-                uint8_t *pool = isk ? P.k_pool : P.v_pool;
-                const int o = 16 * (isk ? p : p - kp);
-                v[q] = *reinterpret_cast<const uint4 *>(pool + s_at[r][isk ? 0 : 2] + o);
-                to[q] = reinterpret_cast<uint4 *>(pool + s_at[r][isk ? 1 : 3] + o);
-            }
-            r += dr;
-            p += dp;
-            if (p >= pieces) {
-                p -= pieces;
-                ++r;
-            }
+    grid_dependency_wait();
+    if (blockIdx.x == 0 && blockIdx.y == 0) finish(P);
+    const size_t rowi = blockIdx.y;
+    const int n = P.counts[rowi], i0 = blockIdx.x * MOVE_ROWS;
+    if (i0 < n) move_chunk<MOVE_THREADS>(P, blockIdx.y / P.Hkv, blockIdx.y % P.Hkv, rowi, i0, n, s_at);
+}
+
+__global__ void __launch_bounds__(MOVE_THREADS) pa_evict_finish_kernel(EvictParams P) {
+    grid_dependency_wait();
+    finish(P);
+}
+
+template <bool FUSED>
+cudaError_t launch_select(const EvictParams &P, dim3 grid, size_t map, cudaStream_t s) {
+    const int ctx = P.max_ctx;
+    if (ctx <= 4096) pa_evict_select_kernel<256, 16, FUSED><<<grid, 256, map, s>>>(P);
+    else if (ctx <= 16384) pa_evict_select_kernel<1024, 16, FUSED><<<grid, 1024, map, s>>>(P);
+    else if (ctx <= 32768) pa_evict_select_kernel<1024, 32, FUSED><<<grid, 1024, map, s>>>(P);
+    else {
+        if (map > 36 * 1024) {
+            const cudaError_t e = cudaFuncSetAttribute(pa_evict_select_kernel<1024, 0, FUSED>,
+                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (1 << 17) + 16);
+            if (e != cudaSuccess) return e;
         }
-#pragma unroll
-        for (int q = 0; q < UN; ++q)
-            if (to[q]) *to[q] = v[q];
+        pa_evict_select_kernel<1024, 0, FUSED><<<grid, 1024, map, s>>>(P);
     }
+    return cudaPeekAtLastError();
 }
 
 }  // namespace evict
@@ -515,21 +555,20 @@ extern "C" PA_API pa_status pa_evict(const pa_problem *p, int32_t budget, int32_
     P.recent = recent;
     P.cap = lo.cap;
     const dim3 grid((unsigned)p->num_kv_heads, (unsigned)p->batch);
-    const int ctx = p->max_context_len;
-    const size_t map = ((size_t)ctx + 31) / 32 * 8 + 16;  // the bitmap of kept slots, the counts before its words
-    if (ctx <= 4096) pa::evict::pa_evict_select_kernel<256, 16><<<grid, 256, map, s>>>(P);
-    else if (ctx <= 16384) pa::evict::pa_evict_select_kernel<1024, 16><<<grid, 1024, map, s>>>(P);
-    else if (ctx <= 32768) pa::evict::pa_evict_select_kernel<1024, 32><<<grid, 1024, map, s>>>(P);
-    else {
-        if (map > 36 * 1024 &&
-            cudaFuncSetAttribute(pa::evict::pa_evict_select_kernel<1024, 0>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (1 << 17) + 16) != cudaSuccess)
-            return PA_ERR_CUDA;
-        pa::evict::pa_evict_select_kernel<1024, 0><<<grid, 1024, map, s>>>(P);
+    const size_t map = ((size_t)p->max_context_len + 31) / 32 * 8 + 16;  // the bitmap of kept slots, the counts before its words
+    // The CTA that selected moves its rows itself while they are one chunk at most (a
+    // decode step: 512 rows of 2064 tokens down to 2048, 14.5 us; 16.4 with a move
+    // kernel); with more, a kernel over all SMs does (128 rows of up to 16384 down to
+    // 2048: 55 us; 68 fused, since a CTA's chunks wait for one another).
+    const bool fused = lo.cap <= pa::evict::MOVE_ROWS;
+    cudaError_t e = fused ? pa::evict::launch_select<true>(P, grid, map, s) : pa::evict::launch_select<false>(P, grid, map, s);
+    if (e != cudaSuccess) return PA_ERR_CUDA;
+    if (fused) {
+        e = pa::launch_pdl(pa::evict::pa_evict_finish_kernel, dim3(1), dim3(pa::evict::MOVE_THREADS), 0, s, P);
+    } else {
+        const unsigned chunks = (unsigned)std::max(1, (lo.cap + pa::evict::MOVE_ROWS - 1) / pa::evict::MOVE_ROWS);
+        e = pa::launch_pdl(pa::evict::pa_evict_move_kernel, dim3(chunks, (unsigned)(p->batch * p->num_kv_heads)),
+                           dim3(pa::evict::MOVE_THREADS), 0, s, P);
     }
-    if (cudaPeekAtLastError() != cudaSuccess) return PA_ERR_CUDA;
-    const unsigned chunks = (unsigned)std::max(1, (lo.cap + pa::evict::MOVE_ROWS - 1) / pa::evict::MOVE_ROWS);
-    const cudaError_t e = pa::launch_pdl(pa::evict::pa_evict_move_kernel, dim3(chunks, (unsigned)(p->batch * p->num_kv_heads)),
-                                         dim3(pa::evict::MOVE_THREADS), 0, s, P);
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
