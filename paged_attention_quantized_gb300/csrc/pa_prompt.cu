@@ -60,6 +60,7 @@ struct PromptParams {
     uint32_t *dev_error;
     int B, total_q, total_k, Hq, Hkv, G;
     int tpt;     // query tokens per 128-row tile: 128 / G
+    unsigned tq_mul;  // floor(2^32 / query tokens per CTA tile) + 1
     int out_dtype, causal;
     const uint16_t *q, *k, *v;  // (for the rows summed again)
     long long qs, ks, vs;       // elements between rows
@@ -119,11 +120,14 @@ struct Lay {
 };
 
 struct Seq {
+    int nt;              // tiles
     int q0, lq, k0, lk;  // lk < 0: the key range breaks the contract; lq = 0 when the query range does
     bool bad;
 };
 
-__device__ __forceinline__ Seq load_seq(const PromptParams &P, int s) {
+__device__ __forceinline__ int per_tile(const PromptParams &P, int x, int tq);
+
+__device__ __forceinline__ Seq load_seq(const PromptParams &P, int s, int tq) {
     Seq r;
     const int a = P.cu_q[s], b = P.cu_q[s + 1], c = P.cu_k[s], d = P.cu_k[s + 1];
     const bool okq = a >= 0 && a <= b && b <= P.total_q, okk = c >= 0 && c <= d && d <= P.total_k;
@@ -131,20 +135,25 @@ __device__ __forceinline__ Seq load_seq(const PromptParams &P, int s) {
     r.lq = okq ? b - a : 0;
     r.k0 = c;
     r.lk = okk ? d - c : -1;
+    r.nt = per_tile(P, r.lq + tq - 1, tq);
     r.bad = !okq || !okk;
     return r;
 }
 
+// x / tq: the high word of a product where that is exact (x * tq < 2^32)
+__device__ __forceinline__ int per_tile(const PromptParams &P, int x, int tq) {
+    return tq > 1 && x < (1 << 24) ? (int)__umulhi((unsigned)x, P.tq_mul) : x / tq;
+}
+
 // tiles of `tq` query tokens that visit at least c blocks of keys: the last
 // `count` of the sequence's nt tiles (blocks grow with the tile)
-__device__ __forceinline__ int tiles_with(int lq, int lk, int c, int tq, int causal) {
-    const int nt = (lq + tq - 1) / tq;
+__device__ __forceinline__ int tiles_with(const PromptParams &P, int lq, int lk, int nt, int c, int tq) {
     if (c <= 0) return nt;
     const int need = (c - 1) * BN;  // visible keys of the tile's last row must exceed this
     if (lk <= need) return 0;
-    if (!causal) return nt;
+    if (!P.causal) return nt;
     const int x = need - (lk - lq);
-    const int first = x < 0 ? 0 : min(x / tq, nt - 1);
+    const int first = x < 0 ? 0 : min(per_tile(P, x, tq), nt - 1);
     return nt - first;
 }
 
@@ -162,28 +171,28 @@ struct Search {
 };
 
 template <typename F>
-__device__ __forceinline__ int over_seqs(const PromptParams &P, const Search &S, F &&f) {
+__device__ __forceinline__ int over_seqs(const PromptParams &P, const Search &S, int TQ, F &&f) {
     const int lane = threadIdx.x & 31;
     int n = 0;
-    for (int s = lane, i = 0; s < P.B; s += 32, ++i) n += f(i == 0 ? S.first[0] : i == 1 ? S.first[1] : load_seq(P, s));
+    for (int s = lane, i = 0; s < P.B; s += 32, ++i) n += f(i == 0 ? S.first[0] : i == 1 ? S.first[1] : load_seq(P, s, TQ));
     return __reduce_add_sync(0xffffffffu, n);
 }
 
-__device__ __forceinline__ Tile find_tile(const PromptParams &P, const Search &S, int TQ, long long idx, int &top) {
+__device__ __forceinline__ Tile find_tile(const PromptParams &P, const Search &S, int TQ, unsigned idx, int &top) {
     const int lane = threadIdx.x & 31;
     Tile t;
     t.seq = -1;
     t.tile = t.q0 = t.lq = t.k0 = t.lk = 0;
-    t.g = (int)(idx % P.Hkv);
-    const long long w = idx / P.Hkv;
-    if (w >= S.tiles) return t;
+    const unsigned w = idx / (unsigned)P.Hkv;  // (tiles of all kv heads are counted in 31 bits, and one round more fits)
+    t.g = (int)(idx - w * (unsigned)P.Hkv);
+    if (w >= (unsigned)S.tiles) return t;
     const int want = (int)w;
     // count(lo) > want >= count(hi) = above; tiles come longest first, so a
     // later one has at most the `top` blocks of the one before
-    int lo = 0, hi = top + 1, above = over_seqs(P, S, [&](const Seq &q) { return tiles_with(q.lq, q.lk, hi, TQ, P.causal); });
+    int lo = 0, hi = top + 1, above = over_seqs(P, S, TQ, [&](const Seq &q) { return tiles_with(P, q.lq, q.lk, q.nt, hi, TQ); });
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        const int n = over_seqs(P, S, [&](const Seq &q) { return tiles_with(q.lq, q.lk, mid, TQ, P.causal); });
+        const int n = over_seqs(P, S, TQ, [&](const Seq &q) { return tiles_with(P, q.lq, q.lk, q.nt, mid, TQ); });
         if (n > want) lo = mid;
         else {
             hi = mid;
@@ -197,13 +206,13 @@ __device__ __forceinline__ Tile find_tile(const PromptParams &P, const Search &S
     for (int base = 0, i = 0; base < P.B; base += 32, ++i) {
         const int s = base + lane;
         Seq q;
-        q.lq = 0;
+        q.lq = q.nt = 0;
         int n = 0, from = 0;
         if (s < P.B) {
-            q = i == 0 ? S.first[0] : i == 1 ? S.first[1] : load_seq(P, s);
-            const int ge = tiles_with(q.lq, q.lk, lo, TQ, P.causal);
-            n = ge - tiles_with(q.lq, q.lk, lo + 1, TQ, P.causal);
-            from = (q.lq + TQ - 1) / TQ - ge;
+            q = i == 0 ? S.first[0] : i == 1 ? S.first[1] : load_seq(P, s, TQ);
+            const int ge = tiles_with(P, q.lq, q.lk, q.nt, lo, TQ);
+            n = ge - tiles_with(P, q.lq, q.lk, q.nt, lo + 1, TQ);
+            from = q.nt - ge;
         }
         int x = n;
 #pragma unroll
@@ -229,9 +238,8 @@ __device__ __forceinline__ Tile find_tile(const PromptParams &P, const Search &S
 }
 
 // position in the order of tiles of this CTA's r-th one: rounds of alternating direction
-__device__ __forceinline__ long long nth_tile(int r) {
-    const long long G = gridDim.x;
-    return r * G + ((r & 1) ? G - 1 - blockIdx.x : blockIdx.x);
+__device__ __forceinline__ unsigned nth_tile(int r) {
+    return (unsigned)r * gridDim.x + ((r & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
 }
 
 template <int D, bool BF16>
@@ -257,19 +265,23 @@ __global__ void __launch_bounds__(THREADS, 1)
     const float NaN = __int_as_float(0x7fc00000);
     const int TQ = P.tpt * QT;
 
-    if (tid == 0) {
-        for (int i = 0; i < Y::NBARS; ++i) {
-            uint32_t c = 1;
-            if (i >= Y::B_P && i < Y::B_P + 2) c = DUAL ? 4 : 8;
-            if (i >= Y::B_OFREE && i < Y::B_OFREE + 2) c = DUAL ? 4 : 8;
-            if (i >= Y::B_INFOFREE && i < Y::B_INFOFREE + NINFO) c = 11;  // load, MMA, look, eight softmax warps
-            if (i >= Y::B_FREE && i < Y::B_FREE + NS) c = 2;                     // MMA, look
-            if (i == Y::B_WG || i == Y::B_EXIT) c = 8;
-            mbar_init(&bars[i], c);
-        }
+    if (tid < Y::NBARS) {
+        const int i = tid;
+        uint32_t c = 1;
+        if (i >= Y::B_P && i < Y::B_P + 2) c = DUAL ? 4 : 8;
+        if (i >= Y::B_OFREE && i < Y::B_OFREE + 2) c = DUAL ? 4 : 8;
+        if (i >= Y::B_INFOFREE && i < Y::B_INFOFREE + NINFO) c = 11;  // load, MMA, look, eight softmax warps
+        if (i >= Y::B_FREE && i < Y::B_FREE + NS) c = 2;              // MMA, look
+        if (i == Y::B_WG || i == Y::B_EXIT) c = 8;
+        mbar_init(&bars[i], c);
+        mbar_fence_init();
+    }
+    if (tid == 128) {
         misc[1] = 0;
         misc[2] = 0;
-        mbar_fence_init();
+        tma_prefetch_desc(&tq);
+        tma_prefetch_desc(&tk);
+        tma_prefetch_desc(&tv);
     }
     if (warp == W_MMA) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sb + Y::MISC_OFF),
@@ -338,17 +350,16 @@ __global__ void __launch_bounds__(THREADS, 1)
             bool bad = false;
             for (int i = 0; i < 2; ++i) {
                 const int s = lane + 32 * i;
-                S.first[i].lq = 0;
-                S.first[i].lk = 0;
-                if (s < P.B) S.first[i] = load_seq(P, s);
+                S.first[i].lq = S.first[i].lk = S.first[i].nt = 0;
+                if (s < P.B) S.first[i] = load_seq(P, s, TQ);
             }
             int longest = 0;
             {
                 int n = 0;
                 for (int s = lane, i = 0; s < P.B; s += 32, ++i) {
-                    const Seq q = i < 2 ? S.first[i] : load_seq(P, s);
+                    const Seq q = i < 2 ? S.first[i] : load_seq(P, s, TQ);
                     bad |= q.bad;
-                    n += (q.lq + TQ - 1) / TQ;
+                    n += q.nt;
                     longest = max(longest, q.lk);
                 }
                 S.tiles = __reduce_add_sync(0xffffffffu, n);
@@ -714,21 +725,36 @@ __global__ void __launch_bounds__(THREADS, 1)
         int wphase = 0, nb = 0, no = 0, u = 0;  // exchanges, blocks, tiles with keys (of this row tile), ring unit
         int rd = 0;
         // one row of the output: o(i) gives 32 channels
+        // (32-byte stores where the base allows them: whole sectors, half the instructions)
+        const bool wide = (reinterpret_cast<uintptr_t>(P.out) & 31) == 0;
         auto write_row = [&](size_t row, int i, const float *o) {
             const size_t e0 = row * D + (DUAL ? 0 : 128 * wg) + 32 * i;
-            if (P.out_dtype == PA_F32) {
-                float4 *d = reinterpret_cast<float4 *>(reinterpret_cast<float *>(P.out) + e0);
+            uint32_t w[32];
+            const bool f32 = P.out_dtype == PA_F32;
+            if (f32) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) d[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(o[e]);
+            } else if (P.out_dtype == PA_BF16) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(o[2 * e], o[2 * e + 1]);
             } else {
-                uint4 *d = reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(P.out) + e0);
-                uint32_t w[16];
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    w[e] = P.out_dtype == PA_BF16 ? pack_bf16x2(o[2 * e], o[2 * e + 1])
-                                                  : pack_f16x2(o[2 * e], o[2 * e + 1]);
+                for (int e = 0; e < 16; ++e) w[e] = pack_f16x2(o[2 * e], o[2 * e + 1]);
+            }
+            uint8_t *d = static_cast<uint8_t *>(P.out) + e0 * (f32 ? 4 : 2);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) d[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+            for (int e = 0; e < 4; ++e) {
+                if (e >= 2 && !f32) break;
+                if (wide) {
+                    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(d + 32 * e), "r"(w[8 * e]),
+                                 "r"(w[8 * e + 1]), "r"(w[8 * e + 2]), "r"(w[8 * e + 3]), "r"(w[8 * e + 4]),
+                                 "r"(w[8 * e + 5]), "r"(w[8 * e + 6]), "r"(w[8 * e + 7])
+                                 : "memory");
+                } else {
+                    *reinterpret_cast<uint4 *>(d + 32 * e) = make_uint4(w[8 * e], w[8 * e + 1], w[8 * e + 2], w[8 * e + 3]);
+                    *reinterpret_cast<uint4 *>(d + 32 * e + 16) =
+                        make_uint4(w[8 * e + 4], w[8 * e + 5], w[8 * e + 6], w[8 * e + 7]);
+                }
             }
         };
         for (;; ++rd) {
@@ -763,7 +789,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (j >= jmask) {
                     const int lim = vis - j * BN - col0;  // columns of this row that count
 #pragma unroll
-                    for (int i = 0; i < NCOL; ++i) s[i] = i < lim ? s[i] : -INFINITY;
+                    for (int q = 0; q < NCOL; q += 32)
+                        if (!__all_sync(0xffffffffu, lim >= q + 32)) {
+#pragma unroll
+                            for (int i = q; i < q + 32; ++i) s[i] = i < lim ? s[i] : -INFINITY;
+                        }
                 }
                 float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
@@ -942,22 +972,28 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                 }
             } else {
+                // (a row that saw nothing: inv = 0, and its sums are 0)
+                const uint64_t inv2 = f2(inv, inv);
+                const float fill = nan_row ? NaN : 0.f;
 #pragma unroll 1
-            for (int i = 0; i < OC / 32; ++i) {
-                float o[32];
-                if (nblk > 0) {
-                    tmem_ld32_nowait(tO + 32u * i, o);
-                    tmem_wait32(o);
-                    if (i == OC / 32 - 1) {  // O may be overwritten by the next tile
-                        tc_fence_before();
-                        warp_arrive(&bars[Y::B_OFREE + x]);
-                    }
-                }
+                for (int i = 0; i < OC / 32; ++i) {
+                    float o[32];
+                    if (nblk > 0) {
+                        tmem_ld32_nowait(tO + 32u * i, o);
+                        tmem_wait32(o);
+                        if (i == OC / 32 - 1) {  // O may be overwritten by the next tile
+                            tc_fence_before();
+                            warp_arrive(&bars[Y::B_OFREE + x]);
+                        }
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = (nblk > 0 && l != 0.f) ? o[e] * inv : (nan_row ? NaN : 0.f);
-                if (live) write_row(row, i, o);
-                __syncwarp();
-            }
+                        for (int e = 0; e < 32; e += 2) f2_split(mul2(f2(o[e], o[e + 1]), inv2), o[e], o[e + 1]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = fill;
+                    }
+                    if (live) write_row(row, i, o);
+                    __syncwarp();
+                }
             }
             warp_arrive(&bars[Y::B_INFOFREE + rd % NINFO]);
         }
@@ -1102,6 +1138,7 @@ extern "C" PA_API pa_status pa_prompt_attention(const pa_prompt_problem *p, cons
     P.Hkv = p->num_kv_heads;
     P.G = G;
     P.tpt = tpt;
+    P.tq_mul = tq_tokens > 1 ? (unsigned)((1ull << 32) / (unsigned)tq_tokens) + 1u : 0u;
     P.out_dtype = p->out_dtype;
     P.causal = p->causal;
     P.q = static_cast<const uint16_t *>(q);
