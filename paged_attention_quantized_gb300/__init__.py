@@ -137,9 +137,17 @@ def fp4_logits(w, p, out, workspace, stream=None) -> None:
                     _ptr(w.block_table), _ptr(workspace), workspace.numel(), _ptr(out), stream_handle(stream))
 
 
-def _dtypes():
-    import torch
-    return {0: torch.float32, 1: torch.float16, 2: torch.bfloat16}
+_late = None  # torch and the binding, imported at the first call that needs them
+
+
+def _torch_and_binding():
+    global _late
+    if _late is None:
+        import torch
+        b = binding()
+        _late = (torch, b, {b.PA_F32: torch.float32, b.PA_F16: torch.float16, b.PA_BF16: torch.bfloat16},
+                 torch.cuda.current_device, torch._C._cuda_getCurrentRawStream)
+    return _late
 
 
 def _need(t, name: str, dtype, numel: int, dev: int) -> int:
@@ -150,13 +158,6 @@ def _need(t, name: str, dtype, numel: int, dev: int) -> int:
         raise ValueError(f"{name}: a contiguous tensor of at least {numel} elements of {dtype or 'any type'} on "
                          f"device {dev} is needed, got {tuple(t.shape)} {t.dtype} on {t.device}, strides {t.stride()}")
     return t.data_ptr()
-
-
-def _here(stream):
-    """(torch, the current CUDA device, the stream's handle); stream None: the current one."""
-    import torch
-    dev = torch.cuda.current_device()
-    return torch, dev, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def prompt_problem(*, num_seqs: int, total_q: int, total_k: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
@@ -181,15 +182,15 @@ def prompt_attention(p, q, k, v, cu_q, cu_k, out, lse=None, dev_error=None, stre
     int32 [num_seqs + 1], out [total_q, Hq, D], lse optional float32
     [total_q, Hq], dev_error an optional int32 tensor of one element that
     collects the error bits."""
-    b = binding()
-    torch, dev, st = _here(stream)
-    types = _dtypes()
+    torch, b, types, device, raw_stream = _torch_and_binding()
+    dev = device()
+    st = raw_stream(dev) if stream is None else stream.cuda_stream
     dt, D, tq, tk, Hq, Hkv = types.get(p.dtype), p.head_dim, p.total_q, p.total_k, p.num_q_heads, p.num_kv_heads
 
     def rows(t, name, heads, stride, n):
-        stride = stride or heads * D
-        if t.get_device() != dev or t.dtype is not dt or t.dim() != 3 or t.shape[0] < n or t.shape[1:] != (heads, D) \
-                or (n > 0 and t.stride() != (stride, D, 1) and not (n == 1 and t.stride()[1:] == (D, 1))):
+        stride, sh, by = stride or heads * D, t.shape, t.stride()
+        if t.get_device() != dev or t.dtype is not dt or len(sh) != 3 or sh[0] < n or sh[1] != heads or sh[2] != D \
+                or (n > 0 and (by[2] != 1 or by[1] != D or (by[0] != stride and n > 1))):
             raise ValueError(f"{name}: [{n}, {heads}, {D}] rows of {dt}, {stride} elements apart, on device {dev} are "
                              f"needed, got {tuple(t.shape)} {t.dtype} on {t.device}, strides {t.stride()}")
         return t.data_ptr()
@@ -208,11 +209,12 @@ def attention_mass(w, p, lse, mass, decay: float = 1.0, dev_error=None, stream=N
     (float32 [B, Hkv, max_context_len]) the softmax weight every cached token
     receives from the query rows w.q, given their log-sum-exps lse
     (float32 [B, n, Hq], as pa_attention wrote them)."""
-    b = binding()
-    torch, dev, st = _here(stream)
+    torch, b, types, device, raw_stream = _torch_and_binding()
+    dev = device()
+    st = raw_stream(dev) if stream is None else stream.cuda_stream
     B, rows = p.batch, p.batch * p.next_n * p.num_q_heads
     i32, f32 = torch.int32, torch.float32
-    b.pa_attention_mass(p, decay, _need(w.q, "q", _dtypes().get(p.q_dtype), rows * p.head_dim_k, dev),
+    b.pa_attention_mass(p, decay, _need(w.q, "q", types.get(p.q_dtype), rows * p.head_dim_k, dev),
                         _need(w.k_pool, "k_pool", None, 1, dev),
                         _need(w.block_table, "block_table", i32, B * p.max_blocks_per_seq, dev),
                         _need(w.context_lens, "context_lens", i32, B, dev),
@@ -234,8 +236,9 @@ def evict(w, p, budget: int, mass, positions, history, mass_out, positions_out, 
     float32 and positions int32 [B, Hkv, max_context_len], history int32
     [B, 2]; the *_out tensors may be the inputs themselves and lens_out
     w.context_lens."""
-    b = binding()
-    torch, dev, st = _here(stream)
+    torch, b, _, device, raw_stream = _torch_and_binding()
+    dev = device()
+    st = raw_stream(dev) if stream is None else stream.cuda_stream
     B, rows = p.batch, p.batch * p.num_kv_heads * p.max_context_len
     i32, f32 = torch.int32, torch.float32
     b.pa_evict(p, budget, sinks, recent, _need(mass, "mass", f32, rows, dev),

@@ -167,6 +167,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) pa_evict_select_kerne
     __shared__ uint64_t s_warp[NW];
     __shared__ uint32_t s_few[32], s_pick, s_err;
     __shared__ int s_cut;
+    grid_dependency_wait();
     const int g = blockIdx.x, b = blockIdx.y;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
@@ -406,6 +407,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) pa_evict_select_kerne
 
 __global__ void __launch_bounds__(MOVE_THREADS) pa_evict_move_kernel(EvictParams P) {
     __shared__ long long s_at[MOVE_ROWS][4];  // K source, K destination, V source, V destination
+    grid_dependents_launch();
     grid_dependency_wait();
     if (blockIdx.x == 0 && blockIdx.y == 0) finish(P);
     const size_t rowi = blockIdx.y;
@@ -414,6 +416,7 @@ __global__ void __launch_bounds__(MOVE_THREADS) pa_evict_move_kernel(EvictParams
 }
 
 __global__ void __launch_bounds__(MOVE_THREADS) pa_evict_finish_kernel(EvictParams P) {
+    grid_dependents_launch();
     grid_dependency_wait();
     finish(P);
 }
@@ -421,18 +424,15 @@ __global__ void __launch_bounds__(MOVE_THREADS) pa_evict_finish_kernel(EvictPara
 template <bool FUSED>
 cudaError_t launch_select(const EvictParams &P, dim3 grid, size_t map, cudaStream_t s) {
     const int ctx = P.max_ctx;
-    if (ctx <= 4096) pa_evict_select_kernel<256, 16, FUSED><<<grid, 256, map, s>>>(P);
-    else if (ctx <= 16384) pa_evict_select_kernel<1024, 16, FUSED><<<grid, 1024, map, s>>>(P);
-    else if (ctx <= 32768) pa_evict_select_kernel<1024, 32, FUSED><<<grid, 1024, map, s>>>(P);
-    else {
-        if (map > 36 * 1024) {
-            const cudaError_t e = cudaFuncSetAttribute(pa_evict_select_kernel<1024, 0, FUSED>,
-                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (1 << 17) + 16);
-            if (e != cudaSuccess) return e;
-        }
-        pa_evict_select_kernel<1024, 0, FUSED><<<grid, 1024, map, s>>>(P);
+    if (ctx <= 4096) return launch_pdl(pa_evict_select_kernel<256, 16, FUSED>, grid, dim3(256), map, s, P);
+    if (ctx <= 16384) return launch_pdl(pa_evict_select_kernel<1024, 16, FUSED>, grid, dim3(1024), map, s, P);
+    if (ctx <= 32768) return launch_pdl(pa_evict_select_kernel<1024, 32, FUSED>, grid, dim3(1024), map, s, P);
+    if (map > 36 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(pa_evict_select_kernel<1024, 0, FUSED>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (1 << 17) + 16);
+        if (e != cudaSuccess) return e;
     }
-    return cudaPeekAtLastError();
+    return launch_pdl(pa_evict_select_kernel<1024, 0, FUSED>, grid, dim3(1024), map, s, P);
 }
 
 }  // namespace evict

@@ -64,6 +64,8 @@ __global__ void __launch_bounds__(THREADS, Shape<D, KV, NB, NT>::CTAS) pa_mass_k
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const float NaN = __int_as_float(0x7fc00000);
 
+    grid_dependents_launch();
+    grid_dependency_wait();
     const bool bad_len = scan_units<THREADS, UT>(P, ps, warp_tot);
     if (bad_len && blockIdx.x == 0 && P.dev_error) atomicOr(P.dev_error, PA_DEV_ERR_CONTEXT_LEN);
     const long long N = (long long)ps[P.B] * P.Hkv;
@@ -339,8 +341,7 @@ cudaError_t launch_rows(const MassParams &P, int sms, cudaStream_t s) {
     // no warp without a unit of the longest possible batch
     const long long units = (long long)P.B * P.Hkv * ((P.max_ctx + UT - 1) / UT);
     const long long ctas = std::min<long long>((long long)sms * per, (units + THREADS / 32 - 1) / (THREADS / 32));
-    pa_mass_kernel<D, KV, NB, NT><<<(unsigned)ctas, THREADS, smem, s>>>(P);
-    return cudaPeekAtLastError();
+    return launch_pdl(pa_mass_kernel<D, KV, NB, NT>, dim3((unsigned)ctas), dim3(THREADS), (size_t)smem, s, P);
 }
 
 template <int D, int KV, int NT>

@@ -143,6 +143,8 @@ __global__ void __launch_bounds__(mtc::THREADS, 1) pa_mass_tc_kernel(MassParams 
         if (tid == 0 && P.dev_error) atomicOr(P.dev_error, PA_DEV_ERR_TIMEOUT);
         return;
     }
+    grid_dependents_launch();
+    grid_dependency_wait();
     const bool bad_len = scan_units<THREADS, CH>(P, ps, misc + 4);
     if (bad_len && blockIdx.x == 0 && P.dev_error) atomicOr(P.dev_error, PA_DEV_ERR_CONTEXT_LEN);
     const long long N = (long long)ps[P.B] * P.Hkv;
@@ -616,8 +618,7 @@ cudaError_t launch_tc(const MassParams &P, int nt, int sms, cudaStream_t s) {
     // no CTA without a tile of the longest possible batch
     const long long tiles = (long long)P.B * P.Hkv * ((P.max_ctx + mtc::CH - 1) / mtc::CH);
     const int ctas = (int)std::max(1ll, std::min<long long>(sms, tiles));
-    pa_mass_tc_kernel<D, KV><<<ctas, mtc::THREADS, smem, s>>>(P, nt, rows_c, chunks, na);
-    return cudaPeekAtLastError();
+    return launch_pdl(pa_mass_tc_kernel<D, KV>, dim3(ctas), dim3(mtc::THREADS), (size_t)smem, s, P, nt, rows_c, chunks, na);
 }
 
 template <int D>

@@ -187,9 +187,11 @@ __device__ __forceinline__ Tile find_tile(const PromptParams &P, const Search &S
     t.g = (int)(idx - w * (unsigned)P.Hkv);
     if (w >= (unsigned)S.tiles) return t;
     const int want = (int)w;
+    // (all tiles in one round of the CTAs: their order does not matter)
+    const bool one_round = (unsigned)S.tiles * (unsigned)P.Hkv <= gridDim.x;
     // count(lo) > want >= count(hi) = above; tiles come longest first, so a
     // later one has at most the `top` blocks of the one before
-    int lo = 0, hi = top + 1, above = over_seqs(P, S, TQ, [&](const Seq &q) { return tiles_with(P, q.lq, q.lk, q.nt, hi, TQ); });
+    int lo = 0, hi = one_round ? 0 : top + 1, above = one_round ? 0 : over_seqs(P, S, TQ, [&](const Seq &q) { return tiles_with(P, q.lq, q.lk, q.nt, hi, TQ); });
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         const int n = over_seqs(P, S, TQ, [&](const Seq &q) { return tiles_with(P, q.lq, q.lk, q.nt, mid, TQ); });
@@ -210,9 +212,12 @@ __device__ __forceinline__ Tile find_tile(const PromptParams &P, const Search &S
         int n = 0, from = 0;
         if (s < P.B) {
             q = i == 0 ? S.first[0] : i == 1 ? S.first[1] : load_seq(P, s, TQ);
-            const int ge = tiles_with(P, q.lq, q.lk, q.nt, lo, TQ);
-            n = ge - tiles_with(P, q.lq, q.lk, q.nt, lo + 1, TQ);
-            from = q.nt - ge;
+            n = q.nt;
+            if (!one_round) {
+                const int ge = tiles_with(P, q.lq, q.lk, q.nt, lo, TQ);
+                n = ge - tiles_with(P, q.lq, q.lk, q.nt, lo + 1, TQ);
+                from = q.nt - ge;
+            }
         }
         int x = n;
 #pragma unroll
@@ -265,6 +270,17 @@ __global__ void __launch_bounds__(THREADS, 1)
     const float NaN = __int_as_float(0x7fc00000);
     const int TQ = P.tpt * QT;
 
+    // set up while the kernel before drains, read nothing of its writes before it has
+    grid_dependents_launch();
+    Search S;  // (the scheduler's: asked for before the barriers are met below)
+    S.first[0].lq = S.first[0].lk = S.first[0].nt = 0;
+    S.first[1] = S.first[0];
+    S.tiles = 0;
+    if (warp == W_SCHED) {
+        grid_dependency_wait();
+        if (lane < P.B) S.first[0] = load_seq(P, lane, TQ);
+        if (lane + 32 < P.B) S.first[1] = load_seq(P, lane + 32, TQ);
+    }
     if (tid < Y::NBARS) {
         const int i = tid;
         uint32_t c = 1;
@@ -289,6 +305,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    grid_dependency_wait();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -346,13 +363,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         regs_dec<REGS_OTHER>();  // the whole third warpgroup
         if (warp == W_SCHED) {
             // ================================================== tiles
-            Search S;
             bool bad = false;
-            for (int i = 0; i < 2; ++i) {
-                const int s = lane + 32 * i;
-                S.first[i].lq = S.first[i].lk = S.first[i].nt = 0;
-                if (s < P.B) S.first[i] = load_seq(P, s, TQ);
-            }
             int longest = 0;
             {
                 int n = 0;
@@ -895,6 +906,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (!ok) break;
             u += 2 * n * NU;
             // ---- output rows
+            ok = sleep_wait(&bars[Y::B_LOOK + rd % NINFO], (rd / NINFO) & 1, abort, err);
+            if (!ok) break;
             if (nblk > 0) {
                 ok = DUAL ? sleep_wait(&bars[Y::B_O + x], no & 1, abort, err)
                           : sleep_wait(&bars[Y::B_O], (nb - 1) & 1, abort, err);
@@ -921,8 +934,6 @@ __global__ void __launch_bounds__(THREADS, 1)
             const float inv = l == 0.f ? 0.f : 1.f / l;
             if (live && P.lse != nullptr && (DUAL || wg == 0))
                 P.lse[row] = nan_row ? NaN : l == 0.f ? -INFINITY : m * P.softmax_scale + logf(l);
-            ok = sleep_wait(&bars[Y::B_LOOK + rd % NINFO], (rd / NINFO) & 1, abort, err);
-            if (!ok) break;
             const bool again =
                 reinterpret_cast<const volatile int *>(smem + Y::INFO_OFF + (rd % NINFO) * 32)[7] != 0 && nblk > 0;
             if (again) {
@@ -1033,6 +1044,10 @@ cudaError_t launch_prompt(const CUtensorMap &tq, const CUtensorMap &tk, const CU
     e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
     const unsigned ctas = (unsigned)std::min<long long>(sms, tiles);
+    // a grid that leaves SMs free may set up on them while the kernel before drains
+    // (two short prompts 7.8 us a call, 9.9 without); one that fills them gains nothing
+    if ((int)ctas < sms)
+        return launch_pdl(pa_prompt_kernel<D, BF16>, dim3(ctas), dim3(THREADS), Lay<D>::SMEM, s, tq, tk, tv, P);
     pa_prompt_kernel<D, BF16><<<ctas, THREADS, Lay<D>::SMEM, s>>>(tq, tk, tv, P);
     return cudaPeekAtLastError();
 }
