@@ -24,7 +24,7 @@
 #include <type_traits>
 
 #include "pa_mass.cuh"
-#include "pa_tc.cuh"
+#include "pa_tc_warp.cuh"
 
 namespace pa {
 namespace mass {

@@ -48,7 +48,7 @@
 #include <type_traits>
 
 #include "pa_attn.cuh"
-#include "pa_tc.cuh"
+#include "pa_tc_warp.cuh"
 
 namespace pa {
 
