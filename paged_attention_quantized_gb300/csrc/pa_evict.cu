@@ -15,6 +15,13 @@
 // Moves (pa_evict_move_kernel, or the selecting CTA when they are few): one thread per 16-byte piece of a moved K or V
 // row.  Sources lie at or past `left`, destinations below it, so no row is
 // read after it was written, whatever the order; HBM bound.
+//
+// Measured on a GB300: 512 rows of 2049-2064 tokens down to 2048 (a decode step)
+// 14 us, all latency (about ten dependent steps of a microsecond); 128 rows of up
+// to 16384 tokens, bf16 head dim 128, down to 2048 52 us (selection 20, moves 29 =
+// 6 TB/s); 256 rows of up to 32768, E4M3 head dim 256, down to 4096 175 us
+// (selection 58, two rounds of the SMs, moves 107 = 5.7 TB/s).  Finding the border
+// key by 32 counted bits instead of digits took the last selection 89 us.
 #include <algorithm>
 #include <cmath>
 

@@ -5,7 +5,11 @@
 //
 // The log-sum-exp is an input, so one pass over K suffices: a token's sum is
 // over rows, not over tokens, and no state is carried between tokens.  HBM
-// bound at decode: every K row is read once.
+// bound at decode: every K row is read once.  Measured on a GB300: one row of
+// 32 / 8 heads over 64 requests of 512-8192 tokens, bf16 head dim 128, 108 us =
+// 6.0 TB/s (0.89 of the measured copy rate); four rows over 32 requests of
+// 1024-32768 tokens, E4M3 head dim 256, 285 us = 4.5 TB/s (0.67: some 400
+// instructions per 16 tokens, half of them conversions).
 //
 // Tokens are the M axis of mma.sync (S^T = K q^T): a warp holds 16 tokens of
 // one (request, kv head), the query rows are N, and a token's sum is a sum

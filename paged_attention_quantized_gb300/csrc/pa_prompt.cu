@@ -32,6 +32,16 @@
 // Copies of the next tile's Q, K and V and its first S run under the end of the
 // current tile.
 //
+// What bounds it.  A block of 128 keys costs a CTA 2048 cycles of the tensor
+// pipe (two row tiles, or one of head dim 256), and at head dim 128 the operands
+// of S alone read shared memory at its full 128 bytes a cycle, beside the copies.
+// Measured on a GB300: one 16384-token prompt, 32 / 8 heads, head dim 128, bf16
+// 1.43 ms = 1.53 PFLOP/s of the visible pairs (0.80 of the measured bf16 rate,
+// about 2700 cycles a block); head dim 256, four prompts of 1024-4096 tokens
+// 0.47 ms = 1.31 PFLOP/s (0.68; copies, S and P.V together ask 2500 cycles a block
+// of shared memory).  What was tried: one row tile per CTA and no persistent loop
+// (1.68 ms), the MMAs issued from a single-lane branch (1.90 ms).
+//
 // Masked keys.  Their scores are replaced by -inf, so P is exactly 0 there; but
 // 0 * NaN is NaN, so their V rows must not meet the product when they hold
 // infinities or NaN.  V rows past the sequence are zeroed in shared memory.  V

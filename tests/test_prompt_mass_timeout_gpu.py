@@ -31,19 +31,20 @@ def nan_or_equal(got, want):
     return bad
 
 for D in (64, 128, 256):
-    lens = [700, 40, 300]
-    T = sum(lens)
+    lens = [700, 40, 300]          # 700 more keys in front of the first: every tile of it has six blocks or more
+    T, TK = sum(lens), sum(lens) + 700
     g = torch.Generator(device="cuda").manual_seed(1)
-    q, k, v = (torch.randn(T, h, D, generator=g, device="cuda").bfloat16() for h in (8, 2, 2))
+    q, k, v = (torch.randn(n, h, D, generator=g, device="cuda").bfloat16() for n, h in ((T, 8), (TK, 2), (TK, 2)))
     cu = torch.tensor([0] + lens).cumsum(0).to(torch.int32).cuda()
-    p = pa.prompt_problem(num_seqs=3, total_q=T, total_k=T, num_q_heads=8, num_kv_heads=2, head_dim=D)
+    ck = torch.tensor([0, 1400, 1440, 1740], dtype=torch.int32).cuda()
+    p = pa.prompt_problem(num_seqs=3, total_q=T, total_k=TK, num_q_heads=8, num_kv_heads=2, head_dim=D)
     want, wl = torch.empty_like(q), torch.empty(T, 8, device="cuda")
-    pa.prompt_attention(p, q, k, v, cu, cu, want, wl)
+    pa.prompt_attention(p, q, k, v, cu, ck, want, wl)
     for unit in (0, 1, 3, 6):
         out, lse = torch.zeros_like(want), torch.zeros_like(wl)
         err = torch.tensor([(unit + 1) << 8], dtype=torch.int32, device="cuda")
         st = lib.pa_prompt_attention(ctypes.byref(p), q.data_ptr(), k.data_ptr(), v.data_ptr(), cu.data_ptr(),
-                                     cu.data_ptr(), out.data_ptr(), lse.data_ptr(), err.data_ptr(), pa.stream_handle())
+                                     ck.data_ptr(), out.data_ptr(), lse.data_ptr(), err.data_ptr(), pa.stream_handle())
         assert st == 0
         torch.cuda.synchronize()
         assert err.item() & 0xFF == b.PA_DEV_ERR_TIMEOUT, (D, unit, err.item())
@@ -51,7 +52,7 @@ for D in (64, 128, 256):
         assert bad.any() and not bad.all(), (D, unit)
         nan_or_equal(lse, wl)
     out, err = torch.zeros_like(want), torch.zeros(1, dtype=torch.int32, device="cuda")
-    pa.prompt_attention(p, q, k, v, cu, cu, out, dev_error=err)
+    pa.prompt_attention(p, q, k, v, cu, ck, out, dev_error=err)
     torch.cuda.synchronize()
     assert err.item() == 0 and torch.equal(out, want)
 
