@@ -485,7 +485,8 @@ PA_API pa_status pa_fp4_logits(const pa_fp4_problem *p, const uint8_t *q, const 
  * num_seqs <= 65535, 16-byte-aligned rows; other problems return
  * PA_ERR_UNSUPPORTED.  A sequence whose prefix sums break the contract
  * (PA_DEV_ERR_CONTEXT_LEN) gets NaN rows when its query range is valid and no
- * rows otherwise; a wait that runs out (PA_DEV_ERR_TIMEOUT) leaves NaN rows.
+ * rows otherwise (no sequence gets any when the ranges together name more rows
+ * than there are); a wait that runs out (PA_DEV_ERR_TIMEOUT) leaves NaN rows.
  * One kernel launch on `stream`, no workspace, no allocation, no
  * synchronisation; results do not depend on how sequences are packed. */
 typedef struct pa_prompt_problem {
@@ -569,7 +570,7 @@ PA_API pa_status pa_attention_mass(const pa_problem *p, float decay, const void 
  * Arguments (device pointers unless stated):
  *  p             host; batch, num_kv_heads, head_dim_k/v, block_size,
  *                num_blocks, max_blocks_per_seq, max_context_len, kv_dtype,
- *                k/v_scale_mode, v_is_k_prefix and num_sms are read.
+ *                k/v_scale_mode and v_is_k_prefix are read.
  *  budget, sinks, recent  host; budget >= 1, sinks + recent <= budget.
  *  mass          [batch][Hkv][max_context_len] fp32.
  *  positions     [batch][Hkv][max_context_len] int32; history [batch][2] int32.

@@ -218,7 +218,9 @@ def attention_mass(w, p, lse, mass, decay: float = 1.0, dev_error=None, stream=N
                         _need(w.k_pool, "k_pool", None, 1, dev),
                         _need(w.block_table, "block_table", i32, B * p.max_blocks_per_seq, dev),
                         _need(w.context_lens, "context_lens", i32, B, dev),
-                        None if w.k_scale is None else _need(w.k_scale, "k_scale", f32, 1, dev),
+                        None if w.k_scale is None else _need(
+                            w.k_scale, "k_scale", f32,
+                            p.num_kv_heads * p.head_dim_k if p.k_scale_mode == b.PA_SCALE_CHANNEL else 1, dev),
                         _need(lse, "lse", f32, rows, dev),
                         _need(mass, "mass", f32, B * p.num_kv_heads * p.max_context_len, dev),
                         None if dev_error is None else _need(dev_error, "dev_error", i32, 1, dev), st)

@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(mtc::THREADS, 1) pa_mass_tc_kernel(MassParams 
         regs_inc<REGS_WORK>();
         // ================================================== loaders: tile i by warpgroup i & 1
         const int wg = warp >> 2, wq = warp & 3;  // the warp's 32 tokens: 32 wq ..
-        int i = wg;                               // the next tile to publish
+        long long i = wg;                         // the next tile to publish
         struct Slot {
             int slot, par;  // buffer, parity of its uses
         };
@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(mtc::THREADS, 1) pa_mass_tc_kernel(MassParams 
             for (int q = 0; q + 1 < QD; ++q) pl[q] = pl[q + 1];
             place(pl[QD - 1]);
         };
-        const int mine = (int)(x1 - x0) * chunks;  // tiles of the CTA, all passes
+        const long long mine = (x1 - x0) * chunks;  // tiles of the CTA, all passes
 #ifdef PA_FAULT_INJECT
         // tile (word >> 8) - 1 of CTA 0 is never published
         const int fi = P.dev_error && blockIdx.x == 0 ? (int)(*P.dev_error >> 8) - 1 : -1;
@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(mtc::THREADS, 1) pa_mass_tc_kernel(MassParams 
         if constexpr (BITS == 16) {
             // up to PF tiles of this warpgroup in flight, then publish the oldest
             const int PF = NA > 2 ? 2 : 1;
-            int ai = wg;          // the next tile to copy
+            long long ai = wg;    // the next tile to copy
             Slot at = {wg, 0};    // its buffer
             while (i < mine) {
                 if (ai < mine && ai - i < 2 * PF) {

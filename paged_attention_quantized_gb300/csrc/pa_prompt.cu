@@ -70,6 +70,7 @@ struct PromptParams {
     uint32_t *dev_error;
     int B, total_q, total_k, Hq, Hkv, G;
     int tpt;     // query tokens per 128-row tile: 128 / G
+    int max_tiles;    // of one kv head, for ascending prefix sums
     unsigned tq_mul;  // floor(2^32 / query tokens per CTA tile) + 1
     int out_dtype, causal;
     const uint16_t *q, *k, *v;  // (for the rows summed again)
@@ -177,18 +178,29 @@ struct Tile {
 // sequences (lane, lane + 32) of this lane.
 struct Search {
     Seq first[2];
-    int tiles;  // of one kv head
+    int tiles;               // of one kv head
+    // where the last tile was found: its number of blocks, the tiles with more and
+    // with as many, the 32 sequences it is among and the tiles of that class before
+    // them.  Tiles are asked for in order, so most are found from here: every CTA
+    // looks through the sequences a few times per number of blocks, not per tile.
+    int top, above, cnt, base, before;
 };
+
+__device__ __forceinline__ void restart(Search &S, int top) {
+    S.top = top;
+    S.above = S.cnt = S.base = S.before = 0;
+}
 
 template <typename F>
 __device__ __forceinline__ int over_seqs(const PromptParams &P, const Search &S, int TQ, F &&f) {
     const int lane = threadIdx.x & 31;
     int n = 0;
+#pragma unroll 4
     for (int s = lane, i = 0; s < P.B; s += 32, ++i) n += f(i == 0 ? S.first[0] : i == 1 ? S.first[1] : load_seq(P, s, TQ));
     return __reduce_add_sync(0xffffffffu, n);
 }
 
-__device__ __forceinline__ Tile find_tile(const PromptParams &P, const Search &S, int TQ, unsigned idx, int &top) {
+__device__ __forceinline__ Tile find_tile(const PromptParams &P, Search &S, int TQ, unsigned idx) {
     const int lane = threadIdx.x & 31;
     Tile t;
     t.seq = -1;
@@ -199,23 +211,32 @@ __device__ __forceinline__ Tile find_tile(const PromptParams &P, const Search &S
     const int want = (int)w;
     // (all tiles in one round of the CTAs: their order does not matter)
     const bool one_round = (unsigned)S.tiles * (unsigned)P.Hkv <= gridDim.x;
-    // count(lo) > want >= count(hi) = above; tiles come longest first, so a
-    // later one has at most the `top` blocks of the one before
-    int lo = 0, hi = one_round ? 0 : top + 1, above = one_round ? 0 : over_seqs(P, S, TQ, [&](const Seq &q) { return tiles_with(P, q.lq, q.lk, q.nt, hi, TQ); });
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        const int n = over_seqs(P, S, TQ, [&](const Seq &q) { return tiles_with(P, q.lq, q.lk, q.nt, mid, TQ); });
-        if (n > want) lo = mid;
-        else {
-            hi = mid;
-            above = n;
+    if (one_round) S.cnt = S.tiles;
+    if (want >= S.cnt) {
+        // another class: count(lo) > want >= count(hi); tiles come longest first, so a
+        // later one has at most the blocks of the one before
+        int lo = 0, hi = S.top + 1;
+        S.cnt = S.tiles;
+        S.above = over_seqs(P, S, TQ, [&](const Seq &q) { return tiles_with(P, q.lq, q.lk, q.nt, hi, TQ); });
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            const int n = over_seqs(P, S, TQ, [&](const Seq &q) { return tiles_with(P, q.lq, q.lk, q.nt, mid, TQ); });
+            if (n > want) {
+                lo = mid;
+                S.cnt = n;
+            } else {
+                hi = mid;
+                S.above = n;
+            }
         }
+        S.top = lo;
+        S.base = S.before = 0;
     }
-    top = lo;
-    // the (want - above)-th, by sequence, of the tiles with exactly lo blocks
-    const int rank = want - above;
-    int before = 0;
-    for (int base = 0, i = 0; base < P.B; base += 32, ++i) {
+    // the (want - above)-th, by sequence, of the tiles with exactly `top` blocks
+    const int rank = want - S.above, lo = S.top;
+    int before = S.before;
+    for (int base = S.base; base < P.B; base += 32) {
+        const int i = base >> 5;
         const int s = base + lane;
         Seq q;
         q.lq = q.nt = 0;
@@ -239,6 +260,8 @@ __device__ __forceinline__ Tile find_tile(const PromptParams &P, const Search &S
         const unsigned mine = __ballot_sync(0xffffffffu, rank >= ex && rank < ex + n);
         if (mine) {
             const int from_lane = __ffs(mine) - 1;
+            S.base = base;
+            S.before = before;
             t.seq = base + from_lane;
             t.tile = __shfl_sync(0xffffffffu, from + rank - ex, from_lane);
             t.q0 = __shfl_sync(0xffffffffu, q.q0, from_lane);
@@ -286,6 +309,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     S.first[0].lq = S.first[0].lk = S.first[0].nt = 0;
     S.first[1] = S.first[0];
     S.tiles = 0;
+    restart(S, 0);
     if (warp == W_SCHED) {
         grid_dependency_wait();
         if (lane < P.B) S.first[0] = load_seq(P, lane, TQ);
@@ -386,12 +410,17 @@ __global__ void __launch_bounds__(THREADS, 1)
                 S.tiles = __reduce_add_sync(0xffffffffu, n);
                 longest = __reduce_max_sync(0xffffffffu, longest);
             }
+            // (prefix sums that go back and forth could name the same rows many times over)
+            if (S.tiles < 0 || S.tiles > P.max_tiles) {
+                S.tiles = 0;
+                bad = true;
+            }
             if (bad && blockIdx.x == 0 && P.dev_error) atomicOr(P.dev_error, PA_DEV_ERR_CONTEXT_LEN);
             const int top0 = (longest + BN - 1) / BN;
-            int top = top0;
+            restart(S, top0);
             bool failed = false;  // a wait ran out: the rows of the tiles not yet written become NaN
             for (int r = 0;; ++r) {
-                const Tile t = find_tile(P, S, TQ, nth_tile(r), top);
+                const Tile t = find_tile(P, S, TQ, nth_tile(r));
                 if (failed) {
                     if (t.seq < 0) break;
                     for (int i = 0; i < TQ && t.tile * TQ + i < t.lq; ++i) {
@@ -425,7 +454,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 failed = true;
                 (void)mbar_wait_bounded(&bars[Y::B_EXIT], 0, nullptr);
                 __syncwarp();
-                top = top0;
+                restart(S, top0);
                 r = back - 1;
             }
         } else if (warp == W_LOAD) {
@@ -1163,6 +1192,7 @@ extern "C" PA_API pa_status pa_prompt_attention(const pa_prompt_problem *p, cons
     P.Hkv = p->num_kv_heads;
     P.G = G;
     P.tpt = tpt;
+    P.max_tiles = (int)(tiles / p->num_kv_heads);
     P.tq_mul = tq_tokens > 1 ? (unsigned)((1ull << 32) / (unsigned)tq_tokens) + 1u : 0u;
     P.out_dtype = p->out_dtype;
     P.causal = p->causal;

@@ -259,3 +259,26 @@ def test_empty_problems_and_wrong_tensors():
         a.update(bad)
         with pytest.raises(ValueError):
             pa.prompt_attention(p, a["q"], a["k"], a["v"], a["cq"], a["ck"], a["out"])
+
+
+@pytest.mark.parametrize("B", [33, 65, 700, 5000])
+def test_many_short_sequences(B):
+    # more sequences than the tile search keeps at hand, of one to three lengths of blocks
+    g = torch.Generator().manual_seed(B)
+    lq = torch.randint(1, 4, (B,), generator=g).tolist()
+    lk = [a + int(x) for a, x in zip(lq, torch.randint(0, 2, (B,), generator=g) * (200 if B < 1000 else 5))]
+    q, k, v, cq, ck = make(lq, lk, 4, 2, 64, "bf16", seed=B)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = call(q, k, v, cq, ck, err=err)
+    assert err.item() == 0
+    check(q, k, v, cq, ck, out, lse)
+
+
+def test_prefix_sums_that_name_rows_over_and_over_are_refused():
+    b = pa.binding()
+    q, k, v, _, _ = make([400], [400], 4, 2, 64, "bf16", seed=1)
+    cu = torch.tensor([0, 400] * 40, dtype=torch.int32)      # 40 times the whole, 39 times backwards
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = call(q, k, v, cu, cu, err=err)
+    assert err.item() == b.PA_DEV_ERR_CONTEXT_LEN
+    assert (out == -77).all() and (lse == -77).all()
