@@ -13,9 +13,10 @@
 //
 // Measured on a GB300: 32 causal rows of 64 / 8 heads (256 rows per kv head) over
 // 16 requests of 2048-16384 tokens, INT8 head dim 128 with per-channel scales
-// 251 us; the two-term products alone are 92 us at the measured bf16 rate, the
+// 182 us; the two-term products alone are 92 us at the measured bf16 rate, the
 // sums (one ex2 per row and token) and the decoding run beside them, and each new
-// (request, kv head) costs the pipeline its staging of the query rows, 5 to 10 us.
+// (request, kv head) costs the pipeline its staging of the query rows, some 6 us
+// (256 rows; 20 us, and 251 us in all, when their terms were packed row by row).
 // The warp-level kernel takes 7.2 ms for the same call; at 16 rows it is the faster
 // one (E4M3 head dim 256: 157 us against 200 us at 24 rows here), hence the border.
 //
@@ -347,13 +348,10 @@ __global__ void __launch_bounds__(mtc::THREADS, 1) pa_mass_tc_kernel(MassParams 
                 fetch_token(u1);
                 // ---- a new segment: its query rows
                 ++seg;
-                if (seg > 0 && !sleep_wait(&bars[Y::B_QFREE], (seg - 1) & 1, abort, err)) {
-                    ok = false;
-                    break;
-                }
                 float *cst = reinterpret_cast<float *>(smem + Y::CST_OFF) + (seg & 1) * (Y::RMAX / 2) * 4;
                 int *vs = reinterpret_cast<int *>(smem + Y::VIS_OFF) + (seg & 1) * Y::RMAX;
                 const float *fold = P.k_mode == PA_SCALE_CHANNEL ? P.k_scale + (size_t)w.g * D : nullptr;
+                const float ks = P.k_mode == PA_SCALE_TENSOR ? P.k_scale[0] : 1.f;
                 const bool scaled = !BF && (fold != nullptr || P.q_dtype == PA_BF16);
                 constexpr int WP = 64 / BITS;  // operand words per raw piece
                 float2 fv[D / 64];
@@ -363,12 +361,23 @@ __global__ void __launch_bounds__(mtc::THREADS, 1) pa_mass_tc_kernel(MassParams 
                     fv[k] = fold ? make_float2(fold[channel_of<BITS>(pc, wd, 0)], fold[channel_of<BITS>(pc, wd, 1)])
                                  : make_float2(1.f, 1.f);
                 }
-                // a warp takes QB rows at a time, all their loads in flight together
-                constexpr int QB = D == 256 ? 4 : 8;
-                for (int rr0 = (warp - W_EPI) * QB; rr0 < rp; rr0 += 8 * QB) {
-                    uint32_t raw[QB][D / 64];  // lane: operand words lane, lane + 32, ... (pairs of channels)
-                    float lse = -INFINITY;
-                    int vis = 0x7FFFFFFF;      // rows past R never count, and do not force the masked sum either
+                // A warp takes QB rows at a time: all their loads in flight together,
+                // and those of its next ones while these are stored.
+                constexpr int QB = D == 256 ? 4 : 8, KW = D / 64;
+                uint32_t raw[QB][KW];  // lane: operand words lane, lane + 32, ... (pairs of channels)
+                float lse;
+                int vis;
+                auto load_rows = [&](int rr0) {
+                    // lane i holds the statistics of row i: one load for all of them (a load
+                    // per row into one register would wait for the row before)
+                    lse = -INFINITY;
+                    vis = 0x7FFFFFFF;  // rows past R never count, and do not force the masked sum either
+                    const int lr = w.c * rows_c + rr0 + lane;
+                    if (lane < QB && rr0 + lane < rows_c && lr < P.R) {
+                        const int lj = lr / P.G;
+                        lse = P.lse[((size_t)w.b * P.n + lj) * P.Hq + w.g * P.G + (lr - lj * P.G)];
+                        vis = P.causal ? w.L - (P.n - 1 - lj) : w.L;
+                    }
                     int r = w.c * rows_c + rr0, j = r / P.G, hg = r - j * P.G;
 #pragma unroll
                     for (int i = 0; i < QB; ++i, ++r) {
@@ -376,7 +385,7 @@ __global__ void __launch_bounds__(mtc::THREADS, 1) pa_mass_tc_kernel(MassParams 
                         const size_t row = ((size_t)w.b * P.n + j) * P.Hq + w.g * P.G + hg;
                         const uint16_t *src = reinterpret_cast<const uint16_t *>(P.q + row * (2 * D));
 #pragma unroll
-                        for (int k = 0; k < D / 64; ++k) {
+                        for (int k = 0; k < KW; ++k) {
                             if constexpr (BITS == 4) {
                                 const int c0 = channel_of<4>((lane + 32 * k) / WP, (lane + 32 * k) % WP, 0);
                                 raw[i][k] = rok ? (uint32_t)src[c0] | ((uint32_t)src[c0 + 4] << 16) : 0u;
@@ -384,79 +393,94 @@ __global__ void __launch_bounds__(mtc::THREADS, 1) pa_mass_tc_kernel(MassParams 
                                 raw[i][k] = rok ? reinterpret_cast<const uint32_t *>(src)[lane + 32 * k] : 0u;
                             }
                         }
-                        if (lane == i && rok) {
-                            lse = P.lse[row];
-                            vis = P.causal ? w.L - (P.n - 1 - j) : w.L;
-                        }
                         if (++hg == P.G) {
                             hg = 0;
                             ++j;
                         }
                     }
-                    auto pair = [&](int i, int k) -> float2 {
-                        const uint32_t x = raw[i][k];
-                        float2 f = P.q_dtype == PA_BF16
-                                       ? make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u))
-                                       : __half22float2(*reinterpret_cast<const __half2 *>(&x));
-                        f.x *= fv[k].x;
-                        f.y *= fv[k].y;
-                        return f;
-                    };
-                    float mx[QB], my_down = 1.f;
+                };
+                int rr0 = (warp - W_EPI) * QB;
+                if (rr0 < rp) load_rows(rr0);
+                if (seg > 0 && !sleep_wait(&bars[Y::B_QFREE], (seg - 1) & 1, abort, err)) {
+                    ok = false;
+                    break;
+                }
+                for (; rr0 < rp; rr0 += 8 * QB) {
+                    float2 v[QB][KW];
+#pragma unroll
+                    for (int i = 0; i < QB; ++i)
+#pragma unroll
+                        for (int k = 0; k < KW; ++k) {
+                            const uint32_t x = raw[i][k];
+                            float2 f = P.q_dtype == PA_BF16
+                                           ? make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u))
+                                           : __half22float2(*reinterpret_cast<const __half2 *>(&x));
+                            f.x *= fv[k].x;
+                            f.y *= fv[k].y;
+                            v[i][k] = f;
+                        }
+                    const float my_lse = lse;
+                    const int my_vis = vis;
+                    if (rr0 + 8 * QB < rp) load_rows(rr0 + 8 * QB);
+                    float my_down = 1.f;
                     if (scaled) {
+                        float mx[QB];
 #pragma unroll
                         for (int i = 0; i < QB; ++i) {
                             mx[i] = 0.f;
 #pragma unroll
-                            for (int k = 0; k < D / 64; ++k) {
-                                const float2 f = pair(i, k);
-                                mx[i] = fmaxf(mx[i], fmaxf(fabsf(f.x), fabsf(f.y)));
-                            }
+                            for (int k = 0; k < KW; ++k)
+                                mx[i] = fmaxf(mx[i], fmaxf(fabsf(v[i][k].x), fabsf(v[i][k].y)));
                         }
 #pragma unroll
                         for (int o = 16; o >= 1; o >>= 1)
 #pragma unroll
                             for (int i = 0; i < QB; ++i) mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], o));
-                    }
 #pragma unroll
-                    for (int i = 0; i < QB; ++i) {
-                        float up = 1.f;
-                        if (scaled) {
+                        for (int i = 0; i < QB; ++i) {
                             int ex = 0;
                             if (mx[i] > 0.f && mx[i] < 3.0e38f) ex = (int)(__float_as_uint(mx[i]) >> 23) - 126;
                             ex = max(-120, min(120, ex));
-                            up = __int_as_float((127 - ex) << 23);
+                            const float up = __int_as_float((127 - ex) << 23);
                             if (lane == i) my_down = __int_as_float((127 + ex) << 23);
-                        }
 #pragma unroll
-                        for (int k = 0; k < D / 64; ++k) {
-                            const int word = lane + 32 * k, c = word >> 2;
-                            const float2 f = pair(i, k);
-                            float a = f.x * up, d = f.y * up;
-                            for (int q = 0; q < nt; ++q) {
-                                const uint32_t x = pack2<BF>(a, d);
-                                *reinterpret_cast<uint32_t *>(smem + q_off + q * rp * D * 2 +
-                                                              op_off(rp, rr0 + i, c) + 4 * (word & 3)) = x;
-                                if constexpr (BF) {
-                                    a -= __uint_as_float(x << 16);
-                                    d -= __uint_as_float(x & 0xFFFF0000u);
-                                } else {
-                                    const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&x));
-                                    a -= h.x;
-                                    d -= h.y;
-                                }
+                            for (int k = 0; k < KW; ++k) {
+                                v[i][k].x *= up;
+                                v[i][k].y *= up;
                             }
                         }
                     }
+                    // term by term, the words of all rows beside one another: word lane + 32 k
+                    // of a row is in 16-byte chunk lane / 4 of channel panel k
+                    uint8_t *dst = smem + q_off + rr0 * 128 + 4 * (lane & 3);
+#pragma unroll 1
+                    for (int q = 0; q < nt; ++q, dst += rp * D * 2) {
+#pragma unroll
+                        for (int i = 0; i < QB; ++i)
+#pragma unroll
+                            for (int k = 0; k < KW; ++k) {
+                                float2 &f = v[i][k];
+                                const uint32_t x = pack2<BF>(f.x, f.y);
+                                *reinterpret_cast<uint32_t *>(dst + k * rp * 128 + i * 128 +
+                                                              (((lane >> 2) ^ ((rr0 + i) & 7)) << 4)) = x;
+                                if constexpr (BF) {
+                                    f.x -= __uint_as_float(x << 16);
+                                    f.y -= __uint_as_float(x & 0xFFFF0000u);
+                                } else {
+                                    const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&x));
+                                    f.x -= h.x;
+                                    f.y -= h.y;
+                                }
+                            }
+                    }
                     if (lane < QB) {
                         const int rr = rr0 + lane;
-                        const float ks = P.k_mode == PA_SCALE_TENSOR ? P.k_scale[0] : 1.f;
-                        const bool on = lse != -INFINITY;
+                        const bool on = my_lse != -INFINITY;
                         // in the exp2 domain: the two roundings by log2 e cost some 2^-24 of a
                         // score or of lse, as much as fp32 scores have anyway
                         cst[(rr >> 1) * 4 + (rr & 1)] = on ? P.softmax_scale * ks * my_down * LOG2E : 0.f;
-                        cst[(rr >> 1) * 4 + 2 + (rr & 1)] = on ? -lse * LOG2E : -INFINITY;
-                        vs[rr] = (vis != 0x7FFFFFFF && !on) ? 0 : vis;
+                        cst[(rr >> 1) * 4 + 2 + (rr & 1)] = on ? -my_lse * LOG2E : -INFINITY;
+                        vs[rr] = (my_vis != 0x7FFFFFFF && !on) ? 0 : my_vis;
                     }
                 }
                 fence_proxy_async_smem();
