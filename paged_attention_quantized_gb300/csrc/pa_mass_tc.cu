@@ -13,7 +13,7 @@
 //
 // Measured on a GB300: 32 causal rows of 64 / 8 heads (256 rows per kv head) over
 // 16 requests of 2048-16384 tokens, INT8 head dim 128 with per-channel scales
-// 182 us; the two-term products alone are 92 us at the measured bf16 rate, the
+// 176 us; the two-term products alone are 92 us at the measured bf16 rate, the
 // sums (one ex2 per row and token) and the decoding run beside them, and each new
 // (request, kv head) costs the pipeline its staging of the query rows, some 6 us
 // (256 rows; 20 us, and 251 us in all, when their terms were packed row by row).
@@ -248,11 +248,18 @@ __global__ void __launch_bounds__(mtc::THREADS, 1) pa_mass_tc_kernel(MassParams 
                 run[h] = q.id[h] >= 1 && q.id[h] < P.num_blocks ? P.k_pool + (size_t)q.id[h] * P.k_block + q.off[h]
                                                                : nullptr;
         };
-        // piece k (of PR) of this lane lies in run k / (PR / 2)
+        // Piece k (of PR) of this lane: piece pq of the warp's token k TK + tq, in run
+        // k / (PR / 2).  A piece becomes OC operand chunks; eight lanes side by side
+        // hold one panel of OC tokens, so that what they store at a time falls into
+        // eight different chunk positions of the swizzle (lanes along a row would
+        // meet two and four at a time).
+        constexpr int OC = 16 / BITS, LP = 8 / OC, TK = 32 / PR;
+        const int tq = (lane >> 3) / (D / 64) * OC + (lane & 7) / LP;
+        const int pq = (lane >> 3) % (D / 64) * LP + (lane & 7) % LP;
         auto piece = [&](int k, int left, bool &live) -> const uint8_t * {
-            const int h = k < PR / 2 ? 0 : 1, q = k * 32 + lane;
-            live = run[h] != nullptr && q / PR < left;
-            return live ? run[h] + (q - h * 16 * PR) * 16 : P.k_pool;
+            const int h = k < PR / 2 ? 0 : 1;
+            live = run[h] != nullptr && k * TK + tq < left;
+            return live ? run[h] + ((k * TK + tq - h * 16) * PR + pq) * 16 : P.k_pool;
         };
         if constexpr (BITS == 16) {
             // up to PF tiles of this warpgroup in flight, then publish the oldest
@@ -269,8 +276,7 @@ __global__ void __launch_bounds__(mtc::THREADS, 1) pa_mass_tc_kernel(MassParams 
                     for (int k = 0; k < PR; ++k) {
                         bool live;
                         const uint8_t *src = piece(k, left, live);
-                        const int q = k * 32 + lane;
-                        cp_async16(dst + op_off(CH, 32 * wq + q / PR, q % PR), src, live);
+                        cp_async16(dst + op_off(CH, 32 * wq + k * TK + tq, pq), src, live);
                     }
                     asm volatile("cp.async.commit_group;" ::: "memory");
                     ai += 2;
@@ -303,15 +309,13 @@ __global__ void __launch_bounds__(mtc::THREADS, 1) pa_mass_tc_kernel(MassParams 
                 const int slot = put.slot;
                 if (i >= NA && !sleep_wait(&bars[Y::B_AFREE + slot], put.par ^ 1, abort, err)) break;
                 uint8_t *dst = smem + Y::A_OFF + slot * Y::A_BYTES;
-                constexpr int OC = 16 / BITS;  // 16-byte operand chunks per raw piece
 #pragma unroll
                 for (int k = 0; k < PR; ++k) {
                     uint32_t wd[4 * OC];
                     decode<KV>(raw[k], wd);
-                    const int q = k * 32 + lane, t = 32 * wq + q / PR, c = (q % PR) * OC;
 #pragma unroll
                     for (int o = 0; o < OC; ++o)
-                        *reinterpret_cast<uint4 *>(dst + op_off(CH, t, c + o)) =
+                        *reinterpret_cast<uint4 *>(dst + op_off(CH, 32 * wq + k * TK + tq, pq * OC + o)) =
                             make_uint4(wd[4 * o], wd[4 * o + 1], wd[4 * o + 2], wd[4 * o + 3]);
                 }
                 fence_proxy_async_smem();
