@@ -13,7 +13,7 @@
 //
 // Measured on a GB300: 32 causal rows of 64 / 8 heads (256 rows per kv head) over
 // 16 requests of 2048-16384 tokens, INT8 head dim 128 with per-channel scales
-// 176 us; the two-term products alone are 92 us at the measured bf16 rate, the
+// 174 us; the two-term products alone are 92 us at the measured bf16 rate, the
 // sums (one ex2 per row and token) and the decoding run beside them, and each new
 // (request, kv head) costs the pipeline its staging of the query rows, some 6 us
 // (256 rows; 20 us, and 251 us in all, when their terms were packed row by row).
@@ -50,7 +50,7 @@ static_assert(512 * REGS_WORK + 128 * REGS_MMA <= THREADS * REGS_LAUNCH, "regist
 
 template <int D>
 struct Lay {
-    static constexpr int NA = D == 64 ? 4 : D == 128 ? 3 : 2;  // A buffers at most
+    static constexpr int NA = D == 64 ? 8 : D == 128 ? 6 : 3;  // A buffers at most
     static constexpr int RMAX = D == 256 ? 128 : 256;          // query rows of a chunk
     static constexpr int A_BYTES = CH * D * 2;
     static constexpr int CST_OFF = 0;                          // [2 segments][RMAX / 2 pairs] {sc0, sc1, -lse0, -lse1}
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(mtc::THREADS, 1) pa_mass_tc_kernel(MassParams 
         struct Place {
             int id[2], off[2], left;  // blocks, byte offsets in them, tokens of the 32 that exist
         };
-        constexpr int QD = 3;
+        constexpr int QD = 2;
         Place pl[QD];
         auto step = [&]() {
             if (!w.end) walk_next(w, P, ps, chunks);
@@ -262,8 +262,12 @@ __global__ void __launch_bounds__(mtc::THREADS, 1) pa_mass_tc_kernel(MassParams 
             return live ? run[h] + ((k * TK + tq - h * 16) * PR + pq) * 16 : P.k_pool;
         };
         if constexpr (BITS == 16) {
-            // up to PF tiles of this warpgroup in flight, then publish the oldest
-            const int PF = NA > 2 ? 2 : 1;
+            // Up to PF tiles of this warpgroup in flight, then publish the oldest.  With
+            // a buffer or two to spare beside the two warpgroups' tiles none waits for
+            // the other's tile before it publishes its own (16 x 2048-16384 f16 tokens,
+            // head dim 128, 96 rows, five buffers: 71 us with two each, 104 with three;
+            // 32 rows, six buffers: 72 with two each, 82 with three).
+            const int PF = NA < 4 ? 1 : (NA - 1) / 2;
             long long ai = wg;    // the next tile to copy
             Slot at = {wg, 0};    // its buffer
             while (i < mine) {
@@ -284,7 +288,9 @@ __global__ void __launch_bounds__(mtc::THREADS, 1) pa_mass_tc_kernel(MassParams 
                     rotate();
                     if (ai < mine && ai - i < 2 * PF) continue;
                 }
-                if (ai - i > 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
+                const long long newer = (ai - i) / 2 - 1;  // copies that may stay in flight
+                if (newer == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+                else if (newer == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
                 else asm volatile("cp.async.wait_group 0;" ::: "memory");
                 fence_proxy_async_smem();
                 if (i != fi) warp_arrive(&bars[Y::B_AFULL + put.slot]);
@@ -293,35 +299,53 @@ __global__ void __launch_bounds__(mtc::THREADS, 1) pa_mass_tc_kernel(MassParams 
             }
             asm volatile("cp.async.wait_group 0;" ::: "memory");
         } else {
-            uint4 raw[PR];
-            auto fetch = [&]() {
+            // The next PF tiles of this warpgroup are on their way in registers, 64 of
+            // them whatever a row's size: with one tile of 8 pieces ahead the loads'
+            // latency bounds few rows (24 rows INT8 head dim 128: 66 us).
+            constexpr int PF = PR >= 16 ? 1 : 16 / PR;
+            uint4 raw[PF][PR];
+            auto fetch = [&](uint4 *to) {
                 const int left = pl[0].left;
                 runs_of(pl[0]);
 #pragma unroll
                 for (int k = 0; k < PR; ++k) {
                     bool live;
                     const uint8_t *src = piece(k, left, live);
-                    raw[k] = live ? __ldg(reinterpret_cast<const uint4 *>(src)) : make_uint4(0u, 0u, 0u, 0u);
+                    to[k] = live ? __ldg(reinterpret_cast<const uint4 *>(src)) : make_uint4(0u, 0u, 0u, 0u);
                 }
             };
-            fetch();
-            for (; i < mine; i += 2, put = two_on(put)) {
-                const int slot = put.slot;
-                if (i >= NA && !sleep_wait(&bars[Y::B_AFREE + slot], put.par ^ 1, abort, err)) break;
-                uint8_t *dst = smem + Y::A_OFF + slot * Y::A_BYTES;
 #pragma unroll
-                for (int k = 0; k < PR; ++k) {
-                    uint32_t wd[4 * OC];
-                    decode<KV>(raw[k], wd);
+            for (int p = 0; p < PF; ++p) {
+                if (p > 0) rotate();
+                fetch(raw[p]);
+            }
+            bool go = true;
+            while (go && i < mine) {
 #pragma unroll
-                    for (int o = 0; o < OC; ++o)
-                        *reinterpret_cast<uint4 *>(dst + op_off(CH, 32 * wq + k * TK + tq, pq * OC + o)) =
-                            make_uint4(wd[4 * o], wd[4 * o + 1], wd[4 * o + 2], wd[4 * o + 3]);
+                for (int p = 0; p < PF; ++p) {
+                    if (!go || i >= mine) break;
+                    const int slot = put.slot;
+                    if (i >= NA && !sleep_wait(&bars[Y::B_AFREE + slot], put.par ^ 1, abort, err)) {
+                        go = false;
+                        break;
+                    }
+                    uint8_t *dst = smem + Y::A_OFF + slot * Y::A_BYTES;
+#pragma unroll
+                    for (int k = 0; k < PR; ++k) {
+                        uint32_t wd[4 * OC];
+                        decode<KV>(raw[p][k], wd);
+#pragma unroll
+                        for (int o = 0; o < OC; ++o)
+                            *reinterpret_cast<uint4 *>(dst + op_off(CH, 32 * wq + k * TK + tq, pq * OC + o)) =
+                                make_uint4(wd[4 * o], wd[4 * o + 1], wd[4 * o + 2], wd[4 * o + 3]);
+                    }
+                    fence_proxy_async_smem();
+                    if (i != fi) warp_arrive(&bars[Y::B_AFULL + slot]);
+                    rotate();
+                    fetch(raw[p]);
+                    i += 2;
+                    put = two_on(put);
                 }
-                fence_proxy_async_smem();
-                if (i != fi) warp_arrive(&bars[Y::B_AFULL + slot]);
-                rotate();
-                fetch();  // the next tile of this warpgroup, while this one is used
             }
         }
     } else if (warp < W_MMA) {
