@@ -7,8 +7,8 @@
 // over rows, not over tokens, and no state is carried between tokens.  HBM
 // bound at decode: every K row is read once.  Measured on a GB300: one row of
 // 32 / 8 heads over 64 requests of 512-8192 tokens, bf16 head dim 128, 108 us =
-// 6.0 TB/s (0.89 of the measured copy rate); four rows over 32 requests of
-// 1024-32768 tokens, E4M3 head dim 256, 285 us = 4.5 TB/s (0.67: some 400
+// 6.0 TB/s (0.89 of the measured copy rate); four tokens (16 rows per
+// kv head) of 32 requests of 1024-32768, E4M3 head dim 256, 285 us = 4.5 TB/s (0.67: some 400
 // instructions per 16 tokens, half of them conversions).
 //
 // Tokens are the M axis of mma.sync (S^T = K q^T): a warp holds 16 tokens of
@@ -350,7 +350,10 @@ cudaError_t launch_rows(const MassParams &P, int sms, cudaStream_t s) {
 
 template <int D, int KV, int NT>
 cudaError_t launch(const MassParams &P, int sms, cudaStream_t s) {
-    return P.R <= 8 ? launch_rows<D, KV, 1, NT>(P, sms, s) : launch_rows<D, KV, 2, NT>(P, sms, s);
+    // (more rows of 16-bit codes of head dims 128 and 256 go to the tensor-core kernel)
+    if constexpr (D == 64 || (KV != PA_F16 && KV != PA_BF16))
+        if (P.R > 8) return launch_rows<D, KV, 2, NT>(P, sms, s);
+    return launch_rows<D, KV, 1, NT>(P, sms, s);
 }
 
 // query terms: a folded per-channel scale, and f16 queries (11 bits) against
@@ -449,7 +452,16 @@ extern "C" PA_API pa_status pa_attention_mass(const pa_problem *p, float decay, 
     P.decay = decay;
     P.softmax_scale = p->softmax_scale;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = P.R > 16   ? pa::mass::launch_mass_tc(P, kv, D, pa::mass::query_terms(P, kv), sms, s)
+    // Past 16 rows the tensor-core kernel; up to 8, and at head dim 64, this one.
+    // Between (16 rows, 8 kv heads, this one / the other): 16-bit codes of head dim
+    // 128 over 64 requests of 512-8192 tokens 156 / 125 us.  Quantized codes cost the
+    // other one its change from (request, kv head) to the next, so it takes them while
+    // they are few: two requests of 37-70 tokens, E4M3 head dim 256, 19.6 / 6.2 us, one
+    // of 20000-32768 39.6 / 23.1, 16 of 2048-16384 118 / 90; 32 of 1024-32768, for two
+    // draws of their lengths, 183 / 182 and 285 / 299; 64 of 512-8192, head dim 128, 84 / 109.
+    const bool few = (long long)P.B * P.Hkv <= sms;
+    const bool tc = P.R > 16 || (P.R > 8 && D > 64 && (kv == PA_F16 || kv == PA_BF16 || few));
+    const cudaError_t e = tc         ? pa::mass::launch_mass_tc(P, kv, D, pa::mass::query_terms(P, kv), sms, s)
                           : D == 64  ? pa::mass::dispatch<64>(P, kv, sms, s)
                           : D == 128 ? pa::mass::dispatch<128>(P, kv, sms, s)
                                      : pa::mass::dispatch<256>(P, kv, sms, s);

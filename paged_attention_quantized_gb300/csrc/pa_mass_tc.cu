@@ -6,23 +6,23 @@
 //   mass[t] += sum over rows of exp(c S^T[t, r] - lse_r)   t < vis_r
 //
 // The warp-level kernel (pa_mass.cu) keeps the query in registers, which
-// holds up to 16 rows; beyond that its operand traffic bounds it.  Here a tile of 128
+// holds up to 16 rows; its operand traffic bounds it there and beyond.  Here a tile of 128
 // tokens is one A operand in shared memory, the rows are one B operand beside
 // it, and the sum over rows needs no shuffles: in tensor memory a token is a
 // lane, so one thread adds up its token's rows.
 //
 // Measured on a GB300: 32 causal rows of 64 / 8 heads (256 rows per kv head) over
 // 16 requests of 2048-16384 tokens, INT8 head dim 128 with per-channel scales
-// 174 us; the two-term products alone are 92 us at the measured bf16 rate, the
+// 173 us; the two-term products alone are 92 us at the measured bf16 rate, the
 // sums (one ex2 per row and token) and the decoding run beside them, and each new
 // (request, kv head) costs the pipeline its staging of the query rows, some 6 us
 // (256 rows; 20 us, and 251 us in all, when their terms were packed row by row).
-// The warp-level kernel takes 7.2 ms for the same call; at 16 rows it is the faster
-// one (E4M3 head dim 256: 157 us against 200 us at 24 rows here), hence the border.
+// The warp-level kernel takes 7.2 ms for the same call; where the border between
+// the two lies, and what they measure there, stands at the entry point beside it.
 //
 // Roles (17 warps at work): two loader warpgroups take alternate tiles -- 16-bit
 // codes are copied asynchronously into the swizzled operand layout, quantized
-// ones loaded a tile ahead into registers, decoded exactly and stored there;
+// ones loaded one to four tiles ahead into registers, decoded exactly and stored there;
 // one warp issues the MMAs; two epilogue warpgroups, one per S^T buffer, sum and
 // update the total (a tile always falls to the same warpgroup, so the passes
 // over chunks of rows are ordered) and stage the query rows of each segment.

@@ -111,7 +111,7 @@ def check(w, lse, decay=1.0, seed=0):
     return want
 
 
-CASES = [  # the warp-level kernel takes up to 16 rows per kv head, the tensor-memory one the others
+CASES = [  # the warp-level kernel takes up to 8 rows per kv head (16 at head dim 64), the tensor-memory one the others
     ("tiny", dict()),
     ("tiny", dict(context_lens=[1, 0, 17, 129])),
     ("bf16", dict(context_lens=[5, 300], Hq=8, Hkv=2)),
@@ -158,6 +158,52 @@ def test_per_token_scales():
         w = token_scaled(W.make("e4m3", context_lens=[70, 131], Hq=8, Hkv=2, D=D, n=n, poison=False))
         w.q = (w.q.float() * 0.2).to(w.q.dtype)
         check(w, scores_lse(w))
+
+
+@pytest.mark.parametrize("num_sms", [0, 1])
+@pytest.mark.parametrize("name,kw", [("e4m3", dict(Hq=8, Hkv=2, n=3, D=256)), ("e4m3", dict(Hq=32, Hkv=2, n=1, D=128)),
+                                     ("int8", dict(Hq=8, Hkv=2, n=4)), ("int4", dict(Hq=18, Hkv=2, n=1)),
+                                     ("bf16", dict(Hq=8, Hkv=2, n=4)), ("bf16", dict(Hq=10, Hkv=2, n=2, D=64))],
+                         ids=lambda x: str(x))
+def test_nine_to_sixteen_rows_on_both_kernels(name, kw, num_sms):
+    # quantized codes of wide heads: the tensor-core kernel while there is at most one
+    # (request, kv head) per SM, the warp-level one with more of them (num_sms = 1)
+    w = tamed(W.make(name, context_lens=[300, 0, 129, 7, 640], **kw))
+    lse = lse_of(w)
+    g = torch.Generator().manual_seed(1)
+    mass = torch.rand(w.B, w.Hkv, w.max_context_len, generator=g)
+    want, top = OE.attention_mass(w, lse, mass, 1.0)
+    d = w.to("cuda")
+    m, err = mass.cuda(), torch.zeros(1, dtype=torch.int32, device="cuda")
+    pa.attention_mass(d, pa.problem(d, num_sms=num_sms), lse.cuda(), m, dev_error=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    got = m.cpu().double().numpy()
+    for b in range(w.B):
+        L = int(w.context_lens[b])
+        tol = bound(w, top, lse, want[b, :, :L] - mass[b, :, :L].double().numpy(), want[b, :, :L])
+        assert (np.abs(got[b, :, :L] - want[b, :, :L]) <= tol).all()
+        assert np.array_equal(got[b, :, L:], mass[b, :, L:].double().numpy())
+
+
+@pytest.mark.parametrize("n", [2, 5, 12, 16, 32])
+def test_long_shares_through_every_buffer(n):
+    # one SM walks every tile: the operand buffers come round many times, with as many
+    # of them as the rows of the query leave room for
+    for name, kw in (("bf16", dict(Hq=16, Hkv=2)), ("int8", dict(Hq=16, Hkv=2)), ("bf16", dict(Hq=16, Hkv=2, D=64))):
+        w = tamed(W.make(name, context_lens=[2300, 1100], n=n, **kw))
+        lse = lse_of(w)
+        mass = torch.zeros(w.B, w.Hkv, w.max_context_len)
+        want, top = OE.attention_mass(w, lse, mass, 1.0)
+        d = w.to("cuda")
+        m = mass.cuda()
+        pa.attention_mass(d, pa.problem(d, num_sms=1), lse.cuda(), m)
+        torch.cuda.synchronize()
+        got = m.cpu().double().numpy()
+        for b in range(w.B):
+            L = int(w.context_lens[b])
+            tol = bound(w, top, lse, want[b, :, :L], want[b, :, :L])
+            assert (np.abs(got[b, :, :L] - want[b, :, :L]) <= tol).all()
 
 
 def test_more_rows_than_a_chunk():
